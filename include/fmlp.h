@@ -320,6 +320,126 @@ FMLP_API fmlp_status fmlp_attn_decode(const void* q, const void* k_new, const vo
                                       size_t workspace_bytes, void* stream);
 
 /*
+ * Packed batches.  The calls below work on the new tokens of B sequences,
+ * packed one sequence after another, and on the KV cache those tokens join:
+ * the same head-major regions as fmlp_attn_decode's.
+ *
+ *   cu_seqlens : int32 [B + 1] on the device: sequence b has the new tokens
+ *                t with cu_seqlens[b] <= t < cu_seqlens[b + 1] (none, one or
+ *                many).  Tokens before cu_seqlens[0] or from cu_seqlens[B] on
+ *                (a padded batch) are passed over: nothing is written for them.
+ *   kv_len     : int32 [B] on the device: the rows that sequence b holds with
+ *                its new tokens, 0 <= kv_len[b] <= n_max.  With n_b new tokens,
+ *                its i-th one stands at position p = kv_len[b] - n_b + i, which
+ *                is also its row of the cache.  A token with p < 0 is padding.
+ *   workspace  : its first 256 bytes (FMLP_CONTROL_BYTES) are control words;
+ *                zero-fill it once.  Read fmlp_device_status as for the other
+ *                calls: a sequence whose kv_len is outside [0, n_max], or whose
+ *                cu_seqlens decrease or leave [0, T], is not processed (its
+ *                outputs and cache stay as they were) and is reported as
+ *                FMLP_ERR_INVALID_ARG.
+ * The lengths are read on the device only, so a captured graph may be replayed
+ * with other lengths in the same buffers.  All the calls run after the previous
+ * work on `stream`, take H >= 1 query heads and H_kv >= 1 KV heads (at most
+ * 1024) of D in {64, 96, 128} values, 1 <= B <= 65536 sequences,
+ * 0 <= T <= 2^24 tokens and n_max < 2^30 rows, and return
+ * FMLP_ERR_INVALID_ARG before launching anything for arguments outside what
+ * they take.  Pointers are 16-byte aligned (cu_seqlens, kv_len and scales:
+ * 4-byte).
+ */
+#define FMLP_CONTROL_BYTES ((size_t)256)
+
+/*
+ * fmlp_rope -- how q and k are rotated.  The first rotary_dim = R values of a
+ * head (a multiple of 16, at most D; 0 rotates nothing) are taken in R/2 pairs,
+ * (i, i + R/2) or, if `interleaved`, (2i, 2i + 1); pair i is turned by the
+ * angle p f_i and scaled by `amplitude` (1 leaves its length).  With
+ * w_i = theta^(-2i/R) and c = original_ctx:
+ *   FMLP_ROPE_PLAIN   f_i = w_i
+ *   FMLP_ROPE_LINEAR  f_i = w_i / factor
+ *   FMLP_ROPE_BANDS   f_i = m w_i + (1 - m) w_i / factor, with
+ *                     m = clamp((c w_i / 2 pi - low) / (high - low), 0, 1): pairs
+ *                     that turn more than `high` times over c keep their
+ *                     frequency, those under `low` turns are divided
+ *   FMLP_ROPE_YARN    f_i = r w_i / factor + (1 - r) w_i, with
+ *                     r = clamp((i - a) / max(b - a, 0.001), 0, 1),
+ *                     a = max(floor(pair(high)), 0), b = min(ceil(pair(low)), R - 1),
+ *                     pair(n) = R ln(c / (2 pi n)) / (2 ln theta); theta > 1
+ * Fields a scaling does not name are not read.
+ */
+enum { FMLP_ROPE_PLAIN = 0, FMLP_ROPE_LINEAR = 1, FMLP_ROPE_BANDS = 2, FMLP_ROPE_YARN = 3 };
+typedef struct fmlp_rope {
+  double theta;          /* base, > 0 */
+  double factor;         /* > 0 */
+  double low, high;      /* 0 < low < high */
+  double amplitude;      /* finite; 1 unless the scaling asks for another */
+  int64_t original_ctx;  /* >= 1 */
+  int rotary_dim;
+  int interleaved;
+  int scaling;
+} fmlp_rope;
+
+/*
+ * fmlp_rope_append -- what a batch's new tokens need before their attention,
+ * in one pass: per-head norms of q and k (optional), the rotation of q and k,
+ * and the append of the rotated keys and the values to the cache.
+ *
+ *   q, k, v    : bf16, T rows of H, H_kv and H_kv heads of D values; a token's
+ *                row starts q_stride (k_stride, v_stride) elements after the
+ *                one before, a multiple of 8 and at least the row's length, so
+ *                that column ranges of one projection's output will do
+ *   q_gamma,
+ *   k_gamma    : bf16 [D] or NULL (no norm): x <- x / sqrt(mean x^2 + eps) *
+ *                gamma over the D values of each head, before the rotation
+ *   eps        : > 0 and finite (read only if a gamma is given)
+ *   q_out      : bf16 [T x H x D], the rotated queries.  It may be q itself
+ *                (q_stride = H D); it must not overlap q, k or v otherwise.
+ *   k_cache,
+ *   v_cache    : bf16 [B x H_kv x n_max x D]; rows p of the new tokens are
+ *                written, every other row stays as it was
+ * Norms and rotation are computed in f32 (angles in binary64) and rounded to
+ * bf16 once; values are copied.  One launch.
+ */
+FMLP_API fmlp_status fmlp_rope_append(const void* q, int64_t q_stride, const void* k,
+                                      int64_t k_stride, const void* v, int64_t v_stride, int64_t T,
+                                      const int32_t* cu_seqlens, const int32_t* kv_len, int64_t B,
+                                      int H, int H_kv, int D, const fmlp_rope* rope,
+                                      const void* q_gamma, const void* k_gamma, float eps,
+                                      void* q_out, void* k_cache, void* v_cache, int64_t n_max,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fmlp_rope_append_q8 -- the same into an int8 cache, this library's own
+ * format: each row x (D values of one head) is held as one binary32 scale
+ *     s = fl32(max |x| / 127)
+ * and D int8 codes clamp(rint(fl32(x / s)), -127, 127) (0 in a row of zeros),
+ * taken from the f32 values after norm and rotation.  A row stands for
+ * codes * s.
+ *
+ *   k_q, v_q : int8 [B x H_kv x n_max x D]
+ *   k_s, v_s : f32 [B x H_kv x n_max]
+ */
+FMLP_API fmlp_status fmlp_rope_append_q8(const void* q, int64_t q_stride, const void* k,
+                                         int64_t k_stride, const void* v, int64_t v_stride,
+                                         int64_t T, const int32_t* cu_seqlens,
+                                         const int32_t* kv_len, int64_t B, int H, int H_kv, int D,
+                                         const fmlp_rope* rope, const void* q_gamma,
+                                         const void* k_gamma, float eps, void* q_out, void* k_q,
+                                         float* k_s, void* v_q, float* v_s, int64_t n_max,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fmlp_kv_read_q8 -- rows 0..kv_len[b]-1 of every region of an int8 cache as
+ * bf16 (code * scale in f32, rounded once), into bf16 regions of the same
+ * shape; the rows behind stay as they were.  With it, fmlp_attn_prefill runs
+ * on sequences whose cache is held in int8.
+ */
+FMLP_API fmlp_status fmlp_kv_read_q8(const void* k_q, const float* k_s, const void* v_q,
+                                     const float* v_s, const int32_t* kv_len, int64_t B, int H_kv,
+                                     int D, int64_t n_max, void* k_cache, void* v_cache,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * fmlp_device_status -- synchronise `stream`, read the device status word in
  * `workspace` and reset it to zero.  Returns FMLP_ERR_TIMEOUT if a kernel
  * gave up a bounded wait since the last check, FMLP_ERR_INVALID_ARG if a

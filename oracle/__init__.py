@@ -25,6 +25,9 @@ and the gate/up interleave, a pure permutation of rows at tile granularity.
 ``quant.py`` restates the library's own int8 weight format (the pages name
 quantized weight streaming but give no format) and the block on it.
 
+``packed.py`` restates the calls on packed batches (rotation and cache append,
+the int8 cache, causal attention of a prompt).
+
 ``attn.py`` restates the token-phase attention step of the same pages
 (section 三, components 1-2 and Figure 3: GKVC's in-place KV append at the
 Eq(2) address, TPSFLAT's RoPE + QK^T + Softmax + PV).

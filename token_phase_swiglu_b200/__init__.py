@@ -22,7 +22,8 @@ __all__ = [
     "fmlp_last_cuda_error", "fmlp_kernel_launch_count", "fmlp_set_wait_timeout_ns", "fmlp_set_fault_injection",
     "fmlp_forward_noalloc", "NOALLOC_SCRATCH_BYTES", "EXPORTED_SYMBOLS", "fmlp_forward_bf16",
     "fmlp_sum_partials", "fmlp_quantize_q8", "fmlp_forward_q8", "Q8_GROUP",
-    "fmlp_attn_workspace_bytes", "fmlp_attn_decode",
+    "fmlp_attn_workspace_bytes", "fmlp_attn_decode", "FmlpRope", "CONTROL_BYTES", "fmlp_rope_append",
+    "fmlp_rope_append_q8", "fmlp_kv_read_q8",
 ]
 
 FMLP_OK, FMLP_ERR_INVALID_ARG, FMLP_ERR_UNSUPPORTED, FMLP_ERR_CUDA, FMLP_ERR_TIMEOUT = range(5)
@@ -30,6 +31,32 @@ FMLP_OK, FMLP_ERR_INVALID_ARG, FMLP_ERR_UNSUPPORTED, FMLP_ERR_CUDA, FMLP_ERR_TIM
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfmlp.so")
 
 _i64, _sz, _vp, _int, _f32 = ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+
+_i32 = ctypes.c_int
+
+
+class _Rope(ctypes.Structure):   # fmlp_rope in include/fmlp.h
+    _fields_ = [("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("amplitude", ctypes.c_double), ("original_ctx", _i64),
+                ("rotary_dim", _i32), ("interleaved", _i32), ("scaling", _i32)]
+
+
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
+
+
+class FmlpRope:
+    """How q and k are rotated (fmlp_rope in include/fmlp.h): the base, the values of a
+    head that turn, their pairing, and the scaling of the frequencies for long contexts
+    ("none", "linear", "bands" or "yarn")."""
+
+    def __init__(self, theta: float, rotary_dim: int, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, low: float = 1.0, high: float = 4.0,
+                 original_ctx: int = 1, amplitude: float = 1.0):
+        if scaling not in _ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}, got {scaling!r}")
+        self._c = _Rope(theta, factor, low, high, amplitude, original_ctx, rotary_dim,
+                        int(interleaved), _ROPE_SCALINGS[scaling])
+
 
 # name -> (restype, argtypes); mirrors include/fmlp.h
 _SIGNATURES = {
@@ -52,6 +79,12 @@ _SIGNATURES = {
     "fmlp_attn_workspace_bytes": (_sz, [_i64, _int, _int, _int]),
     "fmlp_attn_decode": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _int, _i64, _i64, _f32,
                                 _vp, _vp, _sz, _vp]),
+    "fmlp_rope_append": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _int, _int, _int,
+                                ctypes.POINTER(_Rope), _vp, _vp, _f32, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "fmlp_rope_append_q8": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _int, _int, _int,
+                                   ctypes.POINTER(_Rope), _vp, _vp, _f32, _vp, _vp, _vp, _vp, _vp, _i64, _vp,
+                                   _sz, _vp]),
+    "fmlp_kv_read_q8": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _vp, _vp, _vp, _sz, _vp]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGNATURES)
 
@@ -336,6 +369,121 @@ def fmlp_attn_decode(q, k_new, v_new, k_cache, v_cache, pos, n_ctx: int, theta: 
                                        workspace.numel() * workspace.element_size(),
                                        _stream(stream)),
                   "fmlp_attn_decode")
+
+
+CONTROL_BYTES = 256   # FMLP_CONTROL_BYTES in include/fmlp.h
+
+
+def _check_rows(t, name, heads=None, D=None):
+    """A packed batch's rows [T, heads, D]: bf16, every token's heads contiguous, tokens
+    any stride apart (a column range of a projection's output); returns that stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
+    _bf16(t, name)
+    if t.dim() != 3 or (heads is not None and tuple(t.shape[1:]) != (heads, D)):
+        raise ValueError(f"{name} must have shape [tokens, {heads or 'heads'}, {D or 'D'}], got {tuple(t.shape)}")
+    T, h, d = t.shape
+    if T == 0:
+        return h * d
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a token must be contiguous in {name}")
+    stride = t.stride(0) if T > 1 else h * d
+    if stride < h * d:
+        raise ValueError(f"tokens overlap in {name}")
+    return stride
+
+
+def _check_batch(cu_seqlens, kv_len):
+    if not isinstance(kv_len, torch.Tensor) or kv_len.dim() != 1:
+        raise ValueError("kv_len must be a 1-D tensor, one entry a sequence")
+    B = kv_len.shape[0]
+    _check(kv_len, "kv_len", torch.int32, (B,))
+    if cu_seqlens is not None:
+        _check(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    return B
+
+
+def _append_args(q, k, v, cu_seqlens, kv_len, rope, q_out, k_cache, v_cache, workspace, q_gamma, k_gamma,
+                 cache_dtype):
+    q_stride = _check_rows(q, "q")
+    T, H, D = q.shape
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("the caches must be [B, H_kv, n_max, D]")
+    B = _check_batch(cu_seqlens, kv_len)
+    H_kv, n_max = k_cache.shape[1], k_cache.shape[2]
+    k_stride, v_stride = _check_rows(k, "k", H_kv, D), _check_rows(v, "v", H_kv, D)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"q has {T} tokens, k {k.shape[0]} and v {v.shape[0]}")
+    if not isinstance(rope, FmlpRope):
+        raise TypeError(f"rope must be an FmlpRope, got {type(rope).__name__}")
+    _check(k_cache, "k_cache", cache_dtype, (B, H_kv, n_max, D))
+    _check(v_cache, "v_cache", cache_dtype, (B, H_kv, n_max, D))
+    _check(q_out, "q_out", torch.bfloat16, (T, H, D))
+    _check(q_gamma, "q_gamma", torch.bfloat16, (D,), optional=True)
+    _check(k_gamma, "k_gamma", torch.bfloat16, (D,), optional=True)
+    _check_workspace(workspace, CONTROL_BYTES)
+    return q_stride, k_stride, v_stride, T, B, H, H_kv, D, n_max
+
+
+def fmlp_rope_append(q, k, v, cu_seqlens, kv_len, rope, q_out, k_cache, v_cache, workspace, q_gamma=None,
+                     k_gamma=None, eps: float = 1e-6, stream=None) -> None:
+    """q_out [T, H, D] <- the (normed and) rotated queries of a packed batch's T new tokens; their (normed
+    and) rotated keys and their values into rows kv_len[b] - n_b .. kv_len[b] - 1 of the caches
+    [B, H_kv, n_max, D].  See include/fmlp.h."""
+    qs, ks, vs, T, B, H, H_kv, D, n_max = _append_args(q, k, v, cu_seqlens, kv_len, rope, q_out, k_cache, v_cache,
+                                                       workspace, q_gamma, k_gamma, torch.bfloat16)
+    _on_device(q=q, k=k, v=v, cu_seqlens=cu_seqlens, kv_len=kv_len, q_gamma=q_gamma, k_gamma=k_gamma, q_out=q_out,
+               k_cache=k_cache, v_cache=v_cache, workspace=workspace)
+    _check_status(lib.fmlp_rope_append(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, _ptr(cu_seqlens),
+                                       _ptr(kv_len), B, H, H_kv, D, ctypes.byref(rope._c), _ptr(q_gamma),
+                                       _ptr(k_gamma), eps, _ptr(q_out), _ptr(k_cache), _ptr(v_cache), n_max,
+                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       _stream(stream)),
+                  "fmlp_rope_append")
+
+
+def fmlp_rope_append_q8(q, k, v, cu_seqlens, kv_len, rope, q_out, k_q, k_s, v_q, v_s, workspace, q_gamma=None,
+                        k_gamma=None, eps: float = 1e-6, stream=None) -> None:
+    """fmlp_rope_append into an int8 cache: codes k_q, v_q int8 [B, H_kv, n_max, D] and one scale a row,
+    k_s, v_s f32 [B, H_kv, n_max]."""
+    qs, ks, vs, T, B, H, H_kv, D, n_max = _append_args(q, k, v, cu_seqlens, kv_len, rope, q_out, k_q, v_q, workspace,
+                                                       q_gamma, k_gamma, torch.int8)
+    _check(k_s, "k_s", torch.float32, (B, H_kv, n_max))
+    _check(v_s, "v_s", torch.float32, (B, H_kv, n_max))
+    _on_device(q=q, k=k, v=v, cu_seqlens=cu_seqlens, kv_len=kv_len, q_gamma=q_gamma, k_gamma=k_gamma, q_out=q_out,
+               k_q=k_q, k_s=k_s, v_q=v_q, v_s=v_s, workspace=workspace)
+    _check_status(lib.fmlp_rope_append_q8(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, _ptr(cu_seqlens),
+                                          _ptr(kv_len), B, H, H_kv, D, ctypes.byref(rope._c), _ptr(q_gamma),
+                                          _ptr(k_gamma), eps, _ptr(q_out), _ptr(k_q), _ptr(k_s), _ptr(v_q),
+                                          _ptr(v_s), n_max, _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _stream(stream)),
+                  "fmlp_rope_append_q8")
+
+
+def _check_q8_cache(k_q, k_s, v_q, v_s, B):
+    if not isinstance(k_q, torch.Tensor) or k_q.dim() != 4:
+        raise ValueError("the caches must be [B, H_kv, n_max, D]")
+    _, H_kv, n_max, D = k_q.shape
+    for t, name in ((k_q, "k_q"), (v_q, "v_q")):
+        _check(t, name, torch.int8, (B, H_kv, n_max, D))
+    for t, name in ((k_s, "k_s"), (v_s, "v_s")):
+        _check(t, name, torch.float32, (B, H_kv, n_max))
+    return H_kv, n_max, D
+
+
+def fmlp_kv_read_q8(k_q, k_s, v_q, v_s, kv_len, k_cache, v_cache, workspace, stream=None) -> None:
+    """Rows 0 .. kv_len[b] - 1 of bf16 caches [B, H_kv, n_max, D] <- codes times scales of an int8 cache."""
+    B = _check_batch(None, kv_len)
+    H_kv, n_max, D = _check_q8_cache(k_q, k_s, v_q, v_s, B)
+    _check(k_cache, "k_cache", torch.bfloat16, (B, H_kv, n_max, D))
+    _check(v_cache, "v_cache", torch.bfloat16, (B, H_kv, n_max, D))
+    _check_workspace(workspace, CONTROL_BYTES)
+    _on_device(k_q=k_q, k_s=k_s, v_q=v_q, v_s=v_s, kv_len=kv_len, k_cache=k_cache, v_cache=v_cache,
+               workspace=workspace)
+    _check_status(lib.fmlp_kv_read_q8(_ptr(k_q), _ptr(k_s), _ptr(v_q), _ptr(v_s), _ptr(kv_len), B, H_kv, D, n_max,
+                                      _ptr(k_cache), _ptr(v_cache), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _stream(stream)),
+                  "fmlp_kv_read_q8")
 
 
 NOALLOC_SCRATCH_BYTES = 8 << 20   # FMLP_NOALLOC_SCRATCH_BYTES in include/fmlp.h

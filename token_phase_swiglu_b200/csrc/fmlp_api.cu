@@ -25,9 +25,24 @@ cudaError_t g_info_err[kMaxDevices];
 constexpr int64_t kMaxD = 32768;
 constexpr int64_t kMaxI = 65536;
 constexpr int64_t kMaxAttnBatch = 65536;  // sequences per attention call
+constexpr int kMaxHeads = 1024;
+constexpr int64_t kMaxCacheRows = (int64_t)1 << 30;  // n_max of a packed batch's cache
 
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }  // NULL passes
+
+inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+// Sizes common to the calls on packed batches.
+bool batch_ok(int64_t B, int H, int H_kv, int D, int64_t n_max) {
+  return B >= 1 && B <= kMaxAttnBatch && H >= 1 && H <= kMaxHeads && H_kv >= 1 &&
+         H_kv <= kMaxHeads && (D == 64 || D == 96 || D == 128) && n_max >= 1 &&
+         n_max < kMaxCacheRows;
+}
+bool tokens_ok(int64_t T) { return T >= 0 && T <= (int64_t)1 << 24; }
+bool control_ok(const void* workspace, size_t bytes) {
+  return workspace && aligned16(workspace) && bytes >= FMLP_CONTROL_BYTES;
+}
 
 inline uint32_t* status_word(void* workspace) { return (uint32_t*)workspace; }
 
@@ -448,6 +463,88 @@ fmlp_status fmlp_attn_decode(const void* q, const void* k_new, const void* v_new
   cudaError_t e = launch_attn_decode(q, k_new, v_new, k_cache, v_cache, pos, B, H, H_kv, D,
                                      n_max, (int)n_ctx, theta, out, workspace, *dev,
                                      (cudaStream_t)stream);
+  return e == cudaSuccess ? FMLP_OK : cuda_fail(e);
+}
+
+// Rows of q, k or v: aligned, a stride of whole 16-byte vectors that covers them.
+static bool rows_ok(const void* x, int64_t stride, int64_t row) {
+  return x && aligned16(x) && stride >= row && stride % 8 == 0 && stride <= (int64_t)1 << 30;
+}
+
+static fmlp_status append_impl(const AppendArgs& a, size_t workspace_bytes, void* stream) {
+  if (!batch_ok(a.B, a.H, a.H_kv, a.D, a.n_max) || !tokens_ok(a.T)) return FMLP_ERR_INVALID_ARG;
+  if (!control_ok(a.workspace, workspace_bytes)) return FMLP_ERR_INVALID_ARG;
+  double freq[kMaxRopePairs];
+  if (!rope_frequencies(a.rope, a.D, freq)) return FMLP_ERR_INVALID_ARG;
+  if ((a.q_gamma || a.k_gamma) && !eps_ok(a.eps)) return FMLP_ERR_INVALID_ARG;
+  if (!aligned16(a.q_gamma) || !aligned16(a.k_gamma)) return FMLP_ERR_INVALID_ARG;
+  if (!a.cu_seqlens || !aligned4(a.cu_seqlens) || !a.kv_len || !aligned4(a.kv_len))
+    return FMLP_ERR_INVALID_ARG;
+  if (!a.k_cache || !aligned16(a.k_cache) || !a.v_cache || !aligned16(a.v_cache))
+    return FMLP_ERR_INVALID_ARG;
+  if (a.T == 0) return FMLP_OK;
+  if (!rows_ok(a.q, a.q_stride, (int64_t)a.H * a.D) ||
+      !rows_ok(a.k, a.k_stride, (int64_t)a.H_kv * a.D) ||
+      !rows_ok(a.v, a.v_stride, (int64_t)a.H_kv * a.D) || !a.q_out || !aligned16(a.q_out))
+    return FMLP_ERR_INVALID_ARG;
+  // q_out may be q itself; otherwise it overlaps no row that another thread reads
+  const uintptr_t o0 = (uintptr_t)a.q_out, o1 = o0 + (uintptr_t)a.T * a.H * a.D * 2;
+  const struct { const void* x; int64_t stride, row; } in[3] = {
+      {a.q, a.q_stride, (int64_t)a.H * a.D}, {a.k, a.k_stride, (int64_t)a.H_kv * a.D},
+      {a.v, a.v_stride, (int64_t)a.H_kv * a.D}};
+  for (const auto& x : in) {
+    const uintptr_t x0 = (uintptr_t)x.x, x1 = x0 + (uintptr_t)((a.T - 1) * x.stride + x.row) * 2;
+    const bool same = &x == in && o0 == x0 && x.stride == x.row;
+    if (o0 < x1 && x0 < o1 && !same) return FMLP_ERR_INVALID_ARG;
+  }
+  const DeviceInfo* dev = nullptr;
+  fmlp_status st = device_for_launch(&dev);
+  if (st != FMLP_OK) return st;
+  cudaError_t e = launch_rope_append(a, freq, *dev, (cudaStream_t)stream);
+  return e == cudaSuccess ? FMLP_OK : cuda_fail(e);
+}
+
+fmlp_status fmlp_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, int64_t T, const int32_t* cu_seqlens,
+                             const int32_t* kv_len, int64_t B, int H, int H_kv, int D,
+                             const fmlp_rope* rope, const void* q_gamma, const void* k_gamma,
+                             float eps, void* q_out, void* k_cache, void* v_cache, int64_t n_max,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (!rope) return FMLP_ERR_INVALID_ARG;
+  return append_impl({q, k, v, q_stride, k_stride, v_stride, T, cu_seqlens, kv_len, B, H, H_kv, D,
+                      *rope, q_gamma, k_gamma, eps, q_out, k_cache, v_cache, nullptr, nullptr,
+                      n_max, workspace},
+                     workspace_bytes, stream);
+}
+
+fmlp_status fmlp_rope_append_q8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, int64_t T,
+                                const int32_t* cu_seqlens, const int32_t* kv_len, int64_t B, int H,
+                                int H_kv, int D, const fmlp_rope* rope, const void* q_gamma,
+                                const void* k_gamma, float eps, void* q_out, void* k_q, float* k_s,
+                                void* v_q, float* v_s, int64_t n_max, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (!rope || !k_s || !v_s || !aligned4(k_s) || !aligned4(v_s)) return FMLP_ERR_INVALID_ARG;
+  return append_impl({q, k, v, q_stride, k_stride, v_stride, T, cu_seqlens, kv_len, B, H, H_kv, D,
+                      *rope, q_gamma, k_gamma, eps, q_out, k_q, v_q, k_s, v_s, n_max, workspace},
+                     workspace_bytes, stream);
+}
+
+fmlp_status fmlp_kv_read_q8(const void* k_q, const float* k_s, const void* v_q, const float* v_s,
+                            const int32_t* kv_len, int64_t B, int H_kv, int D, int64_t n_max,
+                            void* k_cache, void* v_cache, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  if (!batch_ok(B, 1, H_kv, D, n_max) || !control_ok(workspace, workspace_bytes))
+    return FMLP_ERR_INVALID_ARG;
+  for (const void* x : {k_q, v_q, (const void*)k_cache, (const void*)v_cache})
+    if (!x || !aligned16(x)) return FMLP_ERR_INVALID_ARG;
+  if (!k_s || !v_s || !kv_len || !aligned4(k_s) || !aligned4(v_s) || !aligned4(kv_len))
+    return FMLP_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  fmlp_status st = device_for_launch(&dev);
+  if (st != FMLP_OK) return st;
+  cudaError_t e = launch_kv_read_q8(k_q, k_s, v_q, v_s, kv_len, B, H_kv, D, n_max, k_cache, v_cache,
+                                    workspace, *dev, (cudaStream_t)stream);
   return e == cudaSuccess ? FMLP_OK : cuda_fail(e);
 }
 

@@ -161,6 +161,32 @@ cudaError_t launch_attn_decode(const void* q, const void* k_new, const void* v_n
                                int D, int64_t n_max, int n_ctx, float theta, float* out,
                                void* workspace, const DeviceInfo& dev, cudaStream_t stream);
 
+// Rotation and cache append of a packed batch, and the int8 cache read back
+// (csrc/kvcache.cu).
+constexpr int kMaxRopePairs = 64;
+// The R/2 frequencies of `r`; false if it is not one the library takes.
+bool rope_frequencies(const fmlp_rope& r, int D, double* freq);
+struct AppendArgs {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride, T;
+  const int32_t *cu_seqlens, *kv_len;
+  int64_t B;
+  int H, H_kv, D;
+  fmlp_rope rope;
+  const void *q_gamma, *k_gamma;
+  float eps;
+  void *q_out, *k_cache, *v_cache;
+  float *k_s, *v_s;  // not null: the caches are int8
+  int64_t n_max;
+  void* workspace;
+};
+cudaError_t launch_rope_append(const AppendArgs& a, const double* freq, const DeviceInfo& dev,
+                               cudaStream_t stream);
+cudaError_t launch_kv_read_q8(const void* k_q, const float* k_s, const void* v_q, const float* v_s,
+                              const int32_t* kv_len, int64_t B, int H_kv, int D, int64_t n_max,
+                              void* k_cache, void* v_cache, void* workspace, const DeviceInfo& dev,
+                              cudaStream_t stream);
+
 // out = residual or zero (for a down GEMM with no gate-up prologue before it).
 cudaError_t launch_out_init(float* out, const void* residual, int64_t M, int64_t d,
                             const DeviceInfo& dev, cudaStream_t stream);
