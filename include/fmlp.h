@@ -440,6 +440,44 @@ FMLP_API fmlp_status fmlp_kv_read_q8(const void* k_q, const float* k_s, const vo
                                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * fmlp_prefill_workspace_bytes -- bytes of the workspace fmlp_attn_prefill
+ * needs for at most T tokens of B sequences (0 if the shape is not taken).  A
+ * workspace of more tokens serves fewer.  Zero-fill it once; the calls leave it
+ * ready for the next one.
+ */
+FMLP_API size_t fmlp_prefill_workspace_bytes(int64_t T, int64_t B, int H, int H_kv, int D);
+
+/*
+ * fmlp_attn_prefill -- causal attention of a packed batch's new tokens over the
+ * cache (after fmlp_rope_append): whole prompts, prompts that continue a held
+ * cache, a few draft tokens a sequence, or one token each.  For the token at
+ * position p of sequence b and each query head h, with KV head g = h / (H / H_kv):
+ *     out_h = softmax(scale * q_h . K_g[0..p]) V_g[0..p]
+ * Tokens whose position is negative see no row and get zeros.
+ *
+ *   q         : bf16, T rows of H heads of D values, q_stride elements apart (a
+ *               multiple of 8, >= H D)
+ *   k_cache,
+ *   v_cache   : bf16 [B x H_kv x n_max x D]; rows 0..kv_len[b]-1 must hold finite
+ *               values, the rows behind may hold anything
+ *   scale     : > 0 and finite (1/sqrt(D) usually)
+ *   out       : bf16 [T x H x D], rounded once from f32 sums; the softmax
+ *               weights are rounded to bf16 for their product with V.  It must
+ *               not overlap q or the caches.  The same bits on every run with
+ *               the same lengths.
+ *   workspace : fmlp_prefill_workspace_bytes(T, B, H, H_kv, D), not shared by
+ *               calls that may overlap on the GPU.  After a call that reported
+ *               FMLP_ERR_TIMEOUT, zero it again before reuse.
+ * H must be a multiple of H_kv, H / H_kv <= 128, B H_kv <= 2^24.  One launch
+ * (tensor cores).
+ */
+FMLP_API fmlp_status fmlp_attn_prefill(const void* q, int64_t q_stride, const void* k_cache,
+                                       const void* v_cache, const int32_t* cu_seqlens,
+                                       const int32_t* kv_len, int64_t T, int64_t B, int H, int H_kv,
+                                       int D, int64_t n_max, float scale, void* out,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * fmlp_device_status -- synchronise `stream`, read the device status word in
  * `workspace` and reset it to zero.  Returns FMLP_ERR_TIMEOUT if a kernel
  * gave up a bounded wait since the last check, FMLP_ERR_INVALID_ARG if a

@@ -96,3 +96,41 @@ def tensors():
 def test_binding_checks(bad, error):
     with pytest.raises(error):
         fm.fmlp_rope_append(**(tensors() | bad))
+
+
+def test_prefill_workspace_and_refusals():
+    L = fm.lib
+    assert L.fmlp_prefill_workspace_bytes(2048, 1, 32, 8, 128) >= 2 * 148 * 2 * 128 * 130 * 4
+    assert L.fmlp_prefill_workspace_bytes(1, 1, 32, 8, 128) < L.fmlp_prefill_workspace_bytes(64, 1, 32, 8, 128)
+    assert L.fmlp_prefill_workspace_bytes(0, 1, 8, 8, 64) > 0
+    for T, B, H, Hkv, D in [(-1, 1, 8, 8, 64), (1, 0, 8, 8, 64), (1, 1, 12, 8, 64), (1, 1, 0, 1, 64), (1, 1, 8, 0, 64),
+                            (1, 1, 8, 8, 80), (1 << 25, 1, 8, 8, 64), (1, 1, 258, 2, 64)]:
+        assert L.fmlp_prefill_workspace_bytes(T, B, H, Hkv, D) == 0
+    big = 1 << 30
+
+    def attend(**kw):
+        a = dict(q=A, qs=256, kc=A << 8, vc=A << 12, cu=A, kv=A, T=4, B=2, H=4, Hkv=2, D=64, n_max=16, scale=0.1,
+                 out=0x900000, ws=A, wsb=big) | kw
+        return L.fmlp_attn_prefill(a["q"], a["qs"], a["kc"], a["vc"], a["cu"], a["kv"], a["T"], a["B"], a["H"],
+                                   a["Hkv"], a["D"], a["n_max"], a["scale"], a["out"], a["ws"], a["wsb"], None)
+    assert attend(T=0, q=None, out=None) == fm.FMLP_OK
+    for bad in (dict(q=None), dict(q=MIS), dict(qs=248), dict(qs=260), dict(kc=None), dict(vc=MIS), dict(cu=None),
+                dict(kv=MIS4), dict(T=-1), dict(B=0), dict(H=3), dict(D=32), dict(n_max=0), dict(scale=0.0),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(out=None), dict(out=MIS), dict(out=A + 16),
+                dict(out=(A << 8) + 32), dict(out=A << 12), dict(ws=None), dict(ws=MIS), dict(wsb=1024),
+                dict(B=65536, H=1024, Hkv=1024)):
+        assert attend(**bad) == fm.FMLP_ERR_INVALID_ARG, bad
+
+
+def test_prefill_binding_checks():
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    good = dict(q=bf(5, 4, 64), k_cache=bf(3, 2, 16, 64), v_cache=bf(3, 2, 16, 64),
+                cu_seqlens=torch.zeros(4, dtype=torch.int32), kv_len=torch.zeros(3, dtype=torch.int32), scale=0.1,
+                out=bf(5, 4, 64), workspace=torch.zeros(1 << 24, dtype=torch.uint8))
+    for bad, error in ((dict(q=torch.zeros(5, 4, 64)), TypeError), (dict(out=bf(5, 4, 65)), ValueError),
+                       (dict(out=torch.zeros(5, 4, 64)), TypeError), (dict(k_cache=bf(3, 2, 64)), ValueError),
+                       (dict(v_cache=bf(3, 2, 17, 64)), ValueError), (dict(kv_len=torch.zeros(2, dtype=torch.int32)), ValueError),
+                       (dict(workspace=torch.zeros(64, dtype=torch.uint8)), ValueError),
+                       (dict(q=bf(5, 3, 64), out=bf(5, 3, 64)), fm.FmlpError), (dict(), ValueError)):
+        with pytest.raises(error):
+            fm.fmlp_attn_prefill(**(good | bad))

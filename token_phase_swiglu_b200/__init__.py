@@ -23,7 +23,7 @@ __all__ = [
     "fmlp_forward_noalloc", "NOALLOC_SCRATCH_BYTES", "EXPORTED_SYMBOLS", "fmlp_forward_bf16",
     "fmlp_sum_partials", "fmlp_quantize_q8", "fmlp_forward_q8", "Q8_GROUP",
     "fmlp_attn_workspace_bytes", "fmlp_attn_decode", "FmlpRope", "CONTROL_BYTES", "fmlp_rope_append",
-    "fmlp_rope_append_q8", "fmlp_kv_read_q8",
+    "fmlp_rope_append_q8", "fmlp_kv_read_q8", "fmlp_prefill_workspace_bytes", "fmlp_attn_prefill",
 ]
 
 FMLP_OK, FMLP_ERR_INVALID_ARG, FMLP_ERR_UNSUPPORTED, FMLP_ERR_CUDA, FMLP_ERR_TIMEOUT = range(5)
@@ -84,6 +84,9 @@ _SIGNATURES = {
     "fmlp_rope_append_q8": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _int, _int, _int,
                                    ctypes.POINTER(_Rope), _vp, _vp, _f32, _vp, _vp, _vp, _vp, _vp, _i64, _vp,
                                    _sz, _vp]),
+    "fmlp_prefill_workspace_bytes": (_sz, [_i64, _i64, _int, _int, _int]),
+    "fmlp_attn_prefill": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _i64, _f32, _vp, _vp,
+                                 _sz, _vp]),
     "fmlp_kv_read_q8": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _vp, _vp, _vp, _sz, _vp]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGNATURES)
@@ -484,6 +487,34 @@ def fmlp_kv_read_q8(k_q, k_s, v_q, v_s, kv_len, k_cache, v_cache, workspace, str
                                       _ptr(k_cache), _ptr(v_cache), _ptr(workspace),
                                       workspace.numel() * workspace.element_size(), _stream(stream)),
                   "fmlp_kv_read_q8")
+
+
+def fmlp_prefill_workspace_bytes(T: int, B: int, H: int, H_kv: int, D: int) -> int:
+    n = lib.fmlp_prefill_workspace_bytes(T, B, H, H_kv, D)
+    if n == 0:
+        raise FmlpError(FMLP_ERR_INVALID_ARG, "fmlp_prefill_workspace_bytes: shape not taken")
+    return n
+
+
+def fmlp_attn_prefill(q, k_cache, v_cache, cu_seqlens, kv_len, scale: float, out, workspace, stream=None) -> None:
+    """out [T, H, D] (bf16) <- causal attention of a packed batch's new tokens (queries q [T, H, D], already
+    rotated) over rows 0 .. position of the caches [B, H_kv, n_max, D].  See include/fmlp.h."""
+    q_stride = _check_rows(q, "q")
+    T, H, D = q.shape
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("the caches must be [B, H_kv, n_max, D]")
+    B = _check_batch(cu_seqlens, kv_len)
+    H_kv, n_max = k_cache.shape[1], k_cache.shape[2]
+    _check(k_cache, "k_cache", torch.bfloat16, (B, H_kv, n_max, D))
+    _check(v_cache, "v_cache", torch.bfloat16, (B, H_kv, n_max, D))
+    _check(out, "out", torch.bfloat16, (T, H, D))
+    _check_workspace(workspace, fmlp_prefill_workspace_bytes(T, B, H, H_kv, D))
+    _on_device(q=q, k_cache=k_cache, v_cache=v_cache, cu_seqlens=cu_seqlens, kv_len=kv_len, out=out,
+               workspace=workspace)
+    _check_status(lib.fmlp_attn_prefill(q.data_ptr(), q_stride, _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens),
+                                        _ptr(kv_len), T, B, H, H_kv, D, n_max, scale, _ptr(out), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _stream(stream)),
+                  "fmlp_attn_prefill")
 
 
 NOALLOC_SCRATCH_BYTES = 8 << 20   # FMLP_NOALLOC_SCRATCH_BYTES in include/fmlp.h

@@ -548,6 +548,47 @@ fmlp_status fmlp_kv_read_q8(const void* k_q, const float* k_s, const void* v_q, 
   return e == cudaSuccess ? FMLP_OK : cuda_fail(e);
 }
 
+static bool overlap(const void* a, uintptr_t a_bytes, const void* b, uintptr_t b_bytes) {
+  return (uintptr_t)a < (uintptr_t)b + b_bytes && (uintptr_t)b < (uintptr_t)a + a_bytes;
+}
+
+size_t fmlp_prefill_workspace_bytes(int64_t T, int64_t B, int H, int H_kv, int D) {
+  if (!batch_ok(B, H, H_kv, D, 1) || !tokens_ok(T) || !prefill_shape_ok(H, H_kv)) return 0;
+  return prefill_layout(T, H, H_kv, D).total;
+}
+
+fmlp_status fmlp_attn_prefill(const void* q, int64_t q_stride, const void* k_cache,
+                              const void* v_cache, const int32_t* cu_seqlens,
+                              const int32_t* kv_len, int64_t T, int64_t B, int H, int H_kv, int D,
+                              int64_t n_max, float scale, void* out, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!batch_ok(B, H, H_kv, D, n_max) || !tokens_ok(T) || !prefill_shape_ok(H, H_kv) ||
+      B * H_kv > (int64_t)1 << 24)
+    return FMLP_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FMLP_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < prefill_layout(T, H, H_kv, D).total)
+    return FMLP_ERR_INVALID_ARG;
+  if (!k_cache || !aligned16(k_cache) || !v_cache || !aligned16(v_cache) || !cu_seqlens ||
+      !aligned4(cu_seqlens) || !kv_len || !aligned4(kv_len))
+    return FMLP_ERR_INVALID_ARG;
+  if (T == 0) return FMLP_OK;
+  const int64_t row = (int64_t)H * D;
+  if (!rows_ok(q, q_stride, row) || !out || !aligned16(out)) return FMLP_ERR_INVALID_ARG;
+  const uintptr_t out_bytes = (uintptr_t)(T * row * 2);
+  const uintptr_t cache_bytes = (uintptr_t)(B * H_kv * n_max * D * 2);
+  if (overlap(out, out_bytes, q, (uintptr_t)((T - 1) * q_stride + row) * 2) ||
+      overlap(out, out_bytes, k_cache, cache_bytes) || overlap(out, out_bytes, v_cache, cache_bytes))
+    return FMLP_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  fmlp_status st = device_for_launch(&dev);
+  if (st != FMLP_OK) return st;
+  cudaError_t e = launch_attn_prefill(q, q_stride, k_cache, v_cache, cu_seqlens, kv_len, T, B, H,
+                                      H_kv, D, n_max, scale, out, workspace, *dev,
+                                      (cudaStream_t)stream);
+  return e == cudaSuccess ? FMLP_OK : cuda_fail(e);
+}
+
 fmlp_status fmlp_device_status(void* workspace, void* stream) {
   if (!workspace || !aligned16(workspace)) return FMLP_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;

@@ -187,6 +187,20 @@ cudaError_t launch_kv_read_q8(const void* k_q, const float* k_s, const void* v_q
                               void* k_cache, void* v_cache, void* workspace, const DeviceInfo& dev,
                               cudaStream_t stream);
 
+// Causal attention of a packed batch over its cache (csrc/prefill.cu).
+struct PrefillLayout {
+  size_t counters = 0;  // arrivals at items split over CTAs (zero between calls)
+  size_t partials = 0;  // f32 pieces of them
+  size_t total = 0;
+};
+bool prefill_shape_ok(int H, int H_kv);
+PrefillLayout prefill_layout(int64_t T, int H, int H_kv, int D);
+cudaError_t launch_attn_prefill(const void* q, int64_t q_stride, const void* k_cache,
+                                const void* v_cache, const int32_t* cu_seqlens,
+                                const int32_t* kv_len, int64_t T, int64_t B, int H, int H_kv, int D,
+                                int64_t n_max, float scale, void* out, void* workspace,
+                                const DeviceInfo& dev, cudaStream_t stream);
+
 // out = residual or zero (for a down GEMM with no gate-up prologue before it).
 cudaError_t launch_out_init(float* out, const void* residual, int64_t M, int64_t d,
                             const DeviceInfo& dev, cudaStream_t stream);

@@ -70,4 +70,23 @@ cudaError_t encode_tmap_kblocks_bf16(CUtensorMap* map, const void* base, uint64_
                                  CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+cudaError_t encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                             const uint64_t* strides, const uint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  cudaError_t e = encoder(&fn);
+  if (e != cudaSuccess) return e;
+  if (rank < 2 || rank > 4) return cudaErrorInvalidValue;
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], elem[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    if (i) st[i - 1] = strides[i - 1];
+  }
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base),
+                  d, st, bx, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace fmlp

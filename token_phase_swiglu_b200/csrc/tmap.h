@@ -33,4 +33,11 @@ cudaError_t encode_tmap_blocks_bf16(CUtensorMap* map, const void* base, uint64_t
                                     uint32_t box_rows, uint32_t box_blocks,
                                     CUtensorMapSwizzle swizzle);
 
+// A bf16 tensor of up to 4 dimensions, innermost (contiguous) first; `strides`
+// are the bytes between neighbours along dimensions 1, 2, ...  The box lands
+// row after row with the 128-byte swizzle (box[0] = 64 columns); elements past
+// a dimension's end read as zero.
+cudaError_t encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                             const uint64_t* strides, const uint32_t* box);
+
 }  // namespace fmlp
