@@ -478,6 +478,40 @@ FMLP_API fmlp_status fmlp_attn_prefill(const void* q, int64_t q_stride, const vo
                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * fmlp_attn_q8_workspace_bytes -- bytes of the workspace fmlp_attn_decode_q8
+ * needs (0 if the shape is not taken).  Zero-fill it once; the calls leave it
+ * ready for the next one, of any B.
+ */
+FMLP_API size_t fmlp_attn_q8_workspace_bytes(int64_t B, int H, int H_kv, int D);
+
+/*
+ * fmlp_attn_decode_q8 -- attention of one token a sequence over an int8 cache
+ * (after fmlp_rope_append_q8 with one new token a sequence):
+ *     out_h = softmax(scale * q_h . K_g[0..kv_len-1]) V_g[0..kv_len-1],
+ * g = h / (H / H_kv), with K and V rows standing for codes * scale.
+ *
+ *   q        : bf16 [B x H x D], already rotated
+ *   k_q, v_q : int8 [B x H_kv x n_max x D] codes
+ *   k_s, v_s : f32 [B x H_kv x n_max] scales, finite and >= 0; codes and scales of
+ *              rows from kv_len[b] on may hold anything
+ *   kv_len   : int32 [B] on the device; 0 gives zeros, a length outside [0, n_max]
+ *              is not processed and reported as FMLP_ERR_INVALID_ARG
+ *   scale    : > 0 and finite
+ *   out      : f32 [B x H x D], of f32 precision: the codes are multiplied exactly
+ *              (integer tensor cores) with queries held to 2^-20 and softmax weights to
+ *              2^-24 of their largest.  The same bits on every run with the same lengths.
+ *   workspace: fmlp_attn_q8_workspace_bytes(B, H, H_kv, D), not shared by calls that
+ *              may overlap on the GPU.  After a call that reported FMLP_ERR_TIMEOUT,
+ *              zero it again before reuse.
+ * H must be a multiple of H_kv, H / H_kv <= 16, B H_kv <= 2^24.  One launch.
+ */
+FMLP_API fmlp_status fmlp_attn_decode_q8(const void* q, const void* k_q, const float* k_s,
+                                         const void* v_q, const float* v_s, const int32_t* kv_len,
+                                         int64_t B, int H, int H_kv, int D, int64_t n_max,
+                                         float scale, float* out, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/*
  * fmlp_device_status -- synchronise `stream`, read the device status word in
  * `workspace` and reset it to zero.  Returns FMLP_ERR_TIMEOUT if a kernel
  * gave up a bounded wait since the last check, FMLP_ERR_INVALID_ARG if a

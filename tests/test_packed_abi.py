@@ -134,3 +134,21 @@ def test_prefill_binding_checks():
                        (dict(q=bf(5, 3, 64), out=bf(5, 3, 64)), fm.FmlpError), (dict(), ValueError)):
         with pytest.raises(error):
             fm.fmlp_attn_prefill(**(good | bad))
+
+
+def test_attn_q8_workspace_and_refusals():
+    L = fm.lib
+    assert L.fmlp_attn_q8_workspace_bytes(1, 32, 8, 128) >= 2 * 148 * 4 * 131 * 4
+    for B, H, Hkv, D in [(0, 8, 8, 64), (1, 12, 8, 64), (1, 0, 1, 64), (1, 8, 8, 80), (1, 34, 2, 64), (70000, 8, 8, 64)]:
+        assert L.fmlp_attn_q8_workspace_bytes(B, H, Hkv, D) == 0
+
+    def attend(**kw):
+        a = dict(q=A, kq=A, ks=A, vq=A, vs=A, kv=A, B=2, H=4, Hkv=2, D=64, n_max=16, scale=0.1, out=0x900000, ws=A,
+                 wsb=1 << 30) | kw
+        return L.fmlp_attn_decode_q8(a["q"], a["kq"], a["ks"], a["vq"], a["vs"], a["kv"], a["B"], a["H"], a["Hkv"],
+                                     a["D"], a["n_max"], a["scale"], a["out"], a["ws"], a["wsb"], None)
+    for bad in (dict(q=None), dict(q=MIS), dict(kq=None), dict(kq=MIS), dict(ks=None), dict(vs=MIS4), dict(vq=MIS),
+                dict(kv=None), dict(kv=MIS4), dict(B=0), dict(H=3), dict(H=34), dict(D=32), dict(n_max=0),
+                dict(scale=-1.0), dict(scale=float("nan")), dict(out=None), dict(out=MIS), dict(out=A + 32),
+                dict(ws=None), dict(wsb=300)):
+        assert attend(**bad) == fm.FMLP_ERR_INVALID_ARG, bad

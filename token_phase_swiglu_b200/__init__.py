@@ -24,6 +24,7 @@ __all__ = [
     "fmlp_sum_partials", "fmlp_quantize_q8", "fmlp_forward_q8", "Q8_GROUP",
     "fmlp_attn_workspace_bytes", "fmlp_attn_decode", "FmlpRope", "CONTROL_BYTES", "fmlp_rope_append",
     "fmlp_rope_append_q8", "fmlp_kv_read_q8", "fmlp_prefill_workspace_bytes", "fmlp_attn_prefill",
+    "fmlp_attn_q8_workspace_bytes", "fmlp_attn_decode_q8",
 ]
 
 FMLP_OK, FMLP_ERR_INVALID_ARG, FMLP_ERR_UNSUPPORTED, FMLP_ERR_CUDA, FMLP_ERR_TIMEOUT = range(5)
@@ -87,6 +88,9 @@ _SIGNATURES = {
     "fmlp_prefill_workspace_bytes": (_sz, [_i64, _i64, _int, _int, _int]),
     "fmlp_attn_prefill": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _i64, _f32, _vp, _vp,
                                  _sz, _vp]),
+    "fmlp_attn_q8_workspace_bytes": (_sz, [_i64, _int, _int, _int]),
+    "fmlp_attn_decode_q8": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _int, _i64, _f32, _vp, _vp, _sz,
+                                   _vp]),
     "fmlp_kv_read_q8": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _vp, _vp, _vp, _sz, _vp]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGNATURES)
@@ -515,6 +519,32 @@ def fmlp_attn_prefill(q, k_cache, v_cache, cu_seqlens, kv_len, scale: float, out
                                         _ptr(kv_len), T, B, H, H_kv, D, n_max, scale, _ptr(out), _ptr(workspace),
                                         workspace.numel() * workspace.element_size(), _stream(stream)),
                   "fmlp_attn_prefill")
+
+
+def fmlp_attn_q8_workspace_bytes(B: int, H: int, H_kv: int, D: int) -> int:
+    n = lib.fmlp_attn_q8_workspace_bytes(B, H, H_kv, D)
+    if n == 0:
+        raise FmlpError(FMLP_ERR_INVALID_ARG, "fmlp_attn_q8_workspace_bytes: shape not taken")
+    return n
+
+
+def fmlp_attn_decode_q8(q, k_q, k_s, v_q, v_s, kv_len, scale: float, out, workspace, stream=None) -> None:
+    """out [B, H, D] (f32) <- attention of one token a sequence (queries q [B, H, D] bf16, already rotated) over
+    rows 0 .. kv_len[b] - 1 of an int8 cache (codes [B, H_kv, n_max, D], scales [B, H_kv, n_max])."""
+    B = _check_batch(None, kv_len)
+    H_kv, n_max, D = _check_q8_cache(k_q, k_s, v_q, v_s, B)
+    _bf16(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [B, H, D], got {tuple(q.shape)}")
+    H = q.shape[1]
+    _check(q, "q", torch.bfloat16, (B, H, D))
+    _check(out, "out", torch.float32, (B, H, D))
+    _check_workspace(workspace, fmlp_attn_q8_workspace_bytes(B, H, H_kv, D))
+    _on_device(q=q, k_q=k_q, k_s=k_s, v_q=v_q, v_s=v_s, kv_len=kv_len, out=out, workspace=workspace)
+    _check_status(lib.fmlp_attn_decode_q8(_ptr(q), _ptr(k_q), _ptr(k_s), _ptr(v_q), _ptr(v_s), _ptr(kv_len), B, H,
+                                          H_kv, D, n_max, scale, _ptr(out), _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _stream(stream)),
+                  "fmlp_attn_decode_q8")
 
 
 NOALLOC_SCRATCH_BYTES = 8 << 20   # FMLP_NOALLOC_SCRATCH_BYTES in include/fmlp.h

@@ -109,6 +109,11 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     if (globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
+// The same by a whole warp, all of whose lanes get the same answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                               volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit_ns, abort));
+}
 // Bulk copy global -> shared of `bytes` (16-byte aligned both sides, bytes % 16
 // == 0); completion is counted as transaction bytes on `bar`.
 __device__ __forceinline__ void bulk_copy_g2s(void* dst, const void* src, uint32_t bytes,
@@ -156,6 +161,13 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// 2^x by the hardware approximation (relative error 2^-22; 0 for x = -inf).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Row of gate row i in the packed gate/up matrix (fmlp_pack): tile t of T

@@ -589,6 +589,35 @@ fmlp_status fmlp_attn_prefill(const void* q, int64_t q_stride, const void* k_cac
   return e == cudaSuccess ? FMLP_OK : cuda_fail(e);
 }
 
+size_t fmlp_attn_q8_workspace_bytes(int64_t B, int H, int H_kv, int D) {
+  if (!batch_ok(B, H, H_kv, D, 1) || !attn_q8_shape_ok(H, H_kv)) return 0;
+  return attn_q8_layout(H, H_kv, D).total;
+}
+
+fmlp_status fmlp_attn_decode_q8(const void* q, const void* k_q, const float* k_s, const void* v_q,
+                                const float* v_s, const int32_t* kv_len, int64_t B, int H, int H_kv,
+                                int D, int64_t n_max, float scale, float* out, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (!batch_ok(B, H, H_kv, D, n_max) || !attn_q8_shape_ok(H, H_kv) ||
+      B * H_kv > (int64_t)1 << 24)
+    return FMLP_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FMLP_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < attn_q8_layout(H, H_kv, D).total)
+    return FMLP_ERR_INVALID_ARG;
+  for (const void* x : {q, k_q, v_q, (const void*)out})
+    if (!x || !aligned16(x)) return FMLP_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)k_s, (const void*)v_s, (const void*)kv_len})
+    if (!x || !aligned4(x)) return FMLP_ERR_INVALID_ARG;
+  if (overlap(out, (uintptr_t)(B * H * D * 4), q, (uintptr_t)(B * H * D * 2)))
+    return FMLP_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  fmlp_status st = device_for_launch(&dev);
+  if (st != FMLP_OK) return st;
+  cudaError_t e = launch_attn_decode_q8(q, k_q, k_s, v_q, v_s, kv_len, B, H, H_kv, D, n_max, scale,
+                                        out, workspace, *dev, (cudaStream_t)stream);
+  return e == cudaSuccess ? FMLP_OK : cuda_fail(e);
+}
+
 fmlp_status fmlp_device_status(void* workspace, void* stream) {
   if (!workspace || !aligned16(workspace)) return FMLP_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;

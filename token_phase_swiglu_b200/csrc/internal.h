@@ -201,6 +201,14 @@ cudaError_t launch_attn_prefill(const void* q, int64_t q_stride, const void* k_c
                                 int64_t n_max, float scale, void* out, void* workspace,
                                 const DeviceInfo& dev, cudaStream_t stream);
 
+// Attention of one token a sequence over an int8 cache (csrc/attn_q8.cu).
+bool attn_q8_shape_ok(int H, int H_kv);
+AttnLayout attn_q8_layout(int H, int H_kv, int D);
+cudaError_t launch_attn_decode_q8(const void* q, const void* k_q, const float* k_s, const void* v_q,
+                                  const float* v_s, const int32_t* kv_len, int64_t B, int H,
+                                  int H_kv, int D, int64_t n_max, float scale, float* out,
+                                  void* workspace, const DeviceInfo& dev, cudaStream_t stream);
+
 // out = residual or zero (for a down GEMM with no gate-up prologue before it).
 cudaError_t launch_out_init(float* out, const void* residual, int64_t M, int64_t d,
                             const DeviceInfo& dev, cudaStream_t stream);

@@ -37,6 +37,7 @@
 // sequence are a sum of rounded-up arithmetic terms, which has a closed form.
 #include "common.cuh"
 #include "internal.h"
+#include "plan.cuh"
 #include "ring.cuh"
 #include "tcgen05.cuh"
 #include "tmap.h"
@@ -87,10 +88,8 @@ struct PfBarriers {
   uint32_t tmem;
   int abort, q_issued, kv_issued;
   int last[2];
-  // plan: the first unit's place
-  int64_t total, first_b, first_prefix;
-  int first_p;
-  int64_t scan[kPfThreads / 32];
+  int first_p;               // pair of this CTA's first unit
+  UnitPlan<kPfThreads> plan;
 };
 static_assert(sizeof(PfBarriers) <= kPfHeader, "header");
 
@@ -168,11 +167,11 @@ struct Walk {
     u = begin;
     u1 = end;
     if (u >= u1) return false;
-    b = sh.first_b;
+    b = sh.plan.first_b;
     s = sequence(pp, b, TP);
     pair = sh.first_p;
     units = pair_units(s, pair, TP);
-    const int64_t local = u - sh.first_prefix - pp.H_kv * units_before(s, pair, TP);
+    const int64_t local = u - sh.plan.first_prefix - pp.H_kv * units_before(s, pair, TP);
     g = (int)(local / units);
     j0 = (int)(local % units);
     j1 = (int)min((int64_t)units, j0 + (u1 - u));
@@ -203,13 +202,6 @@ struct Walk {
     return k ? max(j0, min(j1, units_to(s, first_token(t) + k))) : j0;
   }
 };
-
-__device__ __forceinline__ int64_t pf_begin(int64_t c, int64_t ctas, int64_t units) {
-  return c * units / ctas;
-}
-__device__ __forceinline__ int pf_cta_of(int64_t u, int64_t ctas, int64_t units) {
-  return (int)(((u + 1) * ctas - 1) / units);
-}
 
 __device__ __forceinline__ void tma_load_kv(void* dst, const void* tmap, int x, int y, int z,
                                             uint64_t* bar) {
@@ -262,11 +254,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -309,7 +296,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
     }
     mbar_init(&sh.mma_done, 1);
     sh.abort = sh.q_issued = sh.kv_issued = 0;
-    sh.total = 0;
+    sh.plan.total = 0;
     fence_barrier_init();
   }
   if (warp == kPfMma) tmem_alloc(&sh.tmem, kPfTmemCols);
@@ -317,53 +304,20 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
   grid_launch_dependents();
   grid_dependency_wait();  // every input may come from the previous kernel
 
-  // ---- plan: all units, then the sequence of this CTA's first one ----
-  int64_t mine = 0, first_chunk = 0;
-  for (int64_t b = threadIdx.x; b < p.B; b += kPfThreads) {
-    const Sequence s = sequence(p, b, TP);
-    if (s.bad && blockIdx.x == 0) atomicOr(p.ctl.status, kStatusBadInput);
-    const int64_t n = sequence_units(s, TP, p.H_kv);
-    if (b == threadIdx.x) first_chunk = n;
-    mine += n;
-  }
-  if (mine) atomicAdd((unsigned long long*)&sh.total, (unsigned long long)mine);
-  __syncthreads();
-  const int64_t total = sh.total;
-  const int64_t ctas = min((int64_t)gridDim.x, total);
-  int64_t u0 = 0, u1 = 0;
-  if (blockIdx.x < ctas) {
-    u0 = pf_begin(blockIdx.x, ctas, total);
-    u1 = pf_begin(blockIdx.x + 1, ctas, total);
-    int64_t carry = 0;
-    for (int64_t b0 = 0; b0 < p.B && carry <= u0; b0 += kPfThreads) {
-      const int64_t b = b0 + threadIdx.x;
-      const int64_t n = b0 == 0 ? first_chunk
-                        : b < p.B ? sequence_units(sequence(p, b, TP), TP, p.H_kv) : 0;
-      int64_t incl = n;  // inclusive scan over the block
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      __syncthreads();
-      if (lane == 31) sh.scan[warp] = incl;
-      __syncthreads();
-      int64_t before = carry, all = carry;
-      for (int w = 0; w < kPfThreads / 32; ++w) {
-        if (w < warp) before += sh.scan[w];
-        all += sh.scan[w];
-      }
-      const int64_t lo = before + incl - n;
-      if (n && lo <= u0 && u0 < lo + n) {
-        sh.first_b = b;
-        sh.first_prefix = lo;
-      }
-      carry = all;
-    }
-    __syncthreads();
+  int64_t u0, u1;
+  const int64_t ctas = plan_units(
+      sh.plan, p.B,
+      [&](int64_t b, bool first) {
+        const Sequence s = sequence(p, b, TP);
+        if (first && s.bad && blockIdx.x == 0) atomicOr(p.ctl.status, kStatusBadInput);
+        return sequence_units(s, TP, p.H_kv);
+      },
+      u0, u1);
+  const int64_t total = sh.plan.total;
+  if (u0 < u1) {
     if (warp == 0) {  // the pair: a 32-ary search over the closed form
-      const Sequence s = sequence(p, sh.first_b, TP);
-      const int64_t local = u0 - sh.first_prefix;
+      const Sequence s = sequence(p, sh.plan.first_b, TP);
+      const int64_t local = u0 - sh.plan.first_prefix;
       int lo = 0, hi = s.pairs;
       while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32, at = lo + lane * step;
@@ -438,7 +392,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
     constexpr uint32_t kIdescS = idesc_bf16(kTile), kIdescO = idesc_bf16(D) | kTransposeB;
     const uint32_t q_addr = smem_u32(q_smem), kv_addr = smem_u32(kv_smem);
     const auto wait = [&](uint64_t* bar, int phase) {
-      if (mbar_wait_bounded(bar, (uint32_t)(phase & 1), wait_ns, abort)) return true;
+      if (mbar_wait_warp(bar, (uint32_t)(phase & 1), wait_ns, abort)) return true;
       if (lane == 0) {
         sh.abort = 1;
         atomicOr(p.ctl.status, kStatusTimeout);
@@ -543,7 +497,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
       float m = -CUDART_INF_F, l = 0.f;
       bool ok = true;
       for (int j = w.j0; j < jend; ++j) {
-        if (!mbar_wait_bounded(&sh.s_full[t], (uint32_t)(ns & 1), wait_ns, abort)) {
+        if (!mbar_wait_warp(&sh.s_full[t], (uint32_t)(ns & 1), wait_ns, abort)) {
           if (lane == 0) {
             sh.abort = 1;
             atomicOr(p.ctl.status, kStatusTimeout);
@@ -552,7 +506,6 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
           break;
         }
         ++ns;
-        __syncwarp();
         if (warp_ok) {
           tc_fence_after();
           uint32_t s[kTile];
@@ -612,7 +565,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
       }
       const bool any = jend > w.j0;
       if (ok && any) {
-        if (!mbar_wait_bounded(&sh.o_full[t], (uint32_t)(no & 1), wait_ns, abort)) {
+        if (!mbar_wait_warp(&sh.o_full[t], (uint32_t)(no & 1), wait_ns, abort)) {
           if (lane == 0) {
             sh.abort = 1;
             atomicOr(p.ctl.status, kStatusTimeout);
@@ -620,11 +573,10 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
           ok = false;
         }
         ++no;
-        __syncwarp();
       }
       if (consumer_barrier_any<kTile>(1 + t, !ok)) break;
       const int64_t item = w.u - w.j0;
-      const int cf = pf_cta_of(item, ctas, total), cl = pf_cta_of(item + w.units - 1, ctas, total);
+      const int cf = share_of(item, ctas, total), cl = share_of(item + w.units - 1, ctas, total);
       __nv_bfloat16* out =
           p.out + (((int64_t)w.s.c0 + first + tok_r) * p.H + (int64_t)w.g * p.G + head_r) * D;
       // this tile's part of a slot: m, l, then O as float4 [D / 4][rows]

@@ -40,4 +40,9 @@ cudaError_t encode_tmap_blocks_bf16(CUtensorMap* map, const void* base, uint64_t
 cudaError_t encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                              const uint64_t* strides, const uint32_t* box);
 
+// int8 regions of `rows` rows of `cols` bytes (cols <= 128): a box of box_rows x
+// 128 bytes with the 128-byte swizzle; bytes past a row's or region's end read as zero.
+cudaError_t encode_tmap_rows_i8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                                uint64_t regions, uint32_t box_rows);
+
 }  // namespace fmlp
