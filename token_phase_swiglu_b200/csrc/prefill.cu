@@ -59,8 +59,8 @@ constexpr int kPfMaxSlots = 8;
 constexpr int kPfMaxCtas = 256;
 constexpr int kPfHeader = 1024;
 constexpr float kRescaleAbove = 8.f;
-// TMEM columns: S of the two tiles (W over them), O of the two tiles
-constexpr uint32_t kColS = 0, kColO = 256, kPfTmemCols = 512;
+// TMEM columns: S of the two tiles (W over the second half of each), O of the two tiles
+constexpr uint32_t kColS = 0, kColW = 64, kColO = 256, kPfTmemCols = 512;
 
 struct PrefillParams {
   CUtensorMap q_map;   // [T][H_kv][G][D], box TPT x 1 x G x 64
@@ -454,7 +454,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
               const uint32_t v = kv_addr + v_slot * kTileBytes;
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
-                mma_bf16_ta(tmem + kColO + t * kTile, tmem + kColS + t * kTile + k * 8,
+                mma_bf16_ta(tmem + kColO + t * kTile, tmem + kColS + kColW + t * kTile + k * 8,
                             v_desc(v + k * 2048), kIdescO, j > w.j0 || k > 0);
               if (j + 1 >= end[t]) mma_commit(&sh.o_full[t]);
             }
@@ -508,23 +508,32 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
         ++ns;
         if (warp_ok) {
           tc_fence_after();
-          uint32_t s[kTile];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            tmem_ld<32>(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
-          tmem_wait();
+          // S in halves of 64 columns (128 would not fit the registers beside the rest):
+          // the maximum over both, then W of the second half, still held, then of the
+          // first, read again.  W lies over the second half of S.
+          uint32_t s[64];
           const int cols = rows - j * kTile;
-          if (__any_sync(0xffffffffu, cols < kTile)) {
+          const bool cut = __any_sync(0xffffffffu, cols < kTile);
+          const auto load = [&](int c0) {
+            tmem_ld<32>(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld<32>(s_addr + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+            tmem_wait();
+            if (cut) {
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
-              if (i >= cols) s[i] = 0xff800000u;  // -inf
-          }
+              for (int i = 0; i < 64; ++i)
+                if (c0 + i >= cols) s[i] = 0xff800000u;  // -inf
+            }
+          };
           float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-          for (int i = 0; i < kTile; i += 8)
+          for (int half = 0; half < 2; ++half) {
+            load(half * 64);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(s[i + 2 * c]), __uint_as_float(s[i + 2 * c + 1])));
+            for (int i = 0; i < 64; i += 8)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(s[i + 2 * c]), __uint_as_float(s[i + 2 * c + 1])));
+          }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
           if (j == w.j0) {
             m = top;
@@ -547,17 +556,20 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
           const uint64_t sc2 = pk2(p.scale_log2, p.scale_log2), ref2 = pk2(-ref, -ref);
           uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-          for (int i = 0; i < kTile; i += 2) {
-            float x, y;
-            unpk2(ffma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, ref2), x, y);
-            x = ex2(x);
-            y = ex2(y);
-            sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], pk2(x, y));
-            s[i >> 1] = bf16x2(x, y);
+          for (int half = 1; half >= 0; --half) {
+            if (half == 0) load(0);
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              float x, y;
+              unpk2(ffma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, ref2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], pk2(x, y));
+              s[i >> 1] = bf16x2(x, y);
+            }
+            tmem_st32(s_addr + kColW + half * 32, s);
           }
           l += hsum2(fadd2(sum[0], sum[1]));
-          tmem_st32(s_addr, &s[0]);
-          tmem_st32(s_addr + 32, &s[32]);
           tmem_st_wait();
           tc_fence_before();
         }
