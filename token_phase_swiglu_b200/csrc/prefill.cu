@@ -29,7 +29,8 @@
 // must match V's type, and the output is bf16 as well.  l sums the unrounded w.
 //
 // Schedule.  The 128-row units of all items (one KV tile against one pair of
-// query tiles) are split evenly and contiguously over the CTAs, so a long cache
+// query tiles) are split evenly and contiguously over the CTAs, a fixed cost for each
+// item's start and end counted with them, so a long cache
 // read by few tokens is spread over the whole GPU and ragged prompts balance.
 // An item cut by a CTA border leaves f32 pieces (m, l, O) in the workspace; the
 // last CTA to finish merges them in order (nobody waits on another CTA).  Every
@@ -59,6 +60,12 @@ constexpr int kPfMaxSlots = 8;
 constexpr int kPfMaxCtas = 256;
 constexpr int kPfHeader = 1024;
 constexpr float kRescaleAbove = 8.f;
+// An item costs its units and, to start (Q, the first K) and to finish (O), about as
+// much as this many more; the shares of the CTAs are counted in both.
+#ifndef PF_ITEM
+#define PF_ITEM 3
+#endif
+constexpr int kPfItemCost = PF_ITEM;
 // TMEM columns: S of the two tiles (W over the second half of each), O of the two tiles
 constexpr uint32_t kColS = 0, kColW = 64, kColO = 256, kPfTmemCols = 512;
 
@@ -140,58 +147,68 @@ __device__ __forceinline__ int units_to(const Sequence& s, int end) {
 __device__ __forceinline__ int pair_units(const Sequence& s, int i, int TP) {
   return max(units_to(s, min((i + 1) * TP, s.n)), 1);
 }
-// Units of the pairs before i (all of them whole): sum of pair_units.
-__device__ __forceinline__ int64_t units_before(const Sequence& s, int i, int TP) {
+// Cost of the items of one KV head before pair i (all of them whole).
+__device__ __forceinline__ int64_t cost_before(const Sequence& s, int i, int TP) {
   const int base = s.len - s.n;  // pair k ends at base + (k + 1) TP
   const int lead = base >= 0 ? 0 : min(i, -base / TP);  // pairs of padding only
-  if (i == lead) return lead;
-  return lead + floor_sum(i - lead, kTile, TP, (int64_t)base + (int64_t)(lead + 1) * TP + kTile - 1);
+  const int64_t fixed = (int64_t)i * kPfItemCost + lead;
+  if (i == lead) return fixed;
+  return fixed + floor_sum(i - lead, kTile, TP, (int64_t)base + (int64_t)(lead + 1) * TP + kTile - 1);
 }
-__device__ __forceinline__ int64_t sequence_units(const Sequence& s, int TP, int H_kv) {
+__device__ __forceinline__ int64_t sequence_cost(const Sequence& s, int TP, int H_kv) {
   if (s.pairs == 0) return 0;
-  return H_kv * (units_before(s, s.pairs - 1, TP) + pair_units(s, s.pairs - 1, TP));
+  return H_kv * (cost_before(s, s.pairs - 1, TP) + pair_units(s, s.pairs - 1, TP) + kPfItemCost);
 }
 
-// Walks the segments (parts of items) of a CTA's unit range.
+// Walks the segments (parts of items) of a CTA's share.  Unit j of an item stands at
+// cost kPfItemCost + j behind the item's start, so a share may hold an item's start and
+// none of its units: such segments are passed over.
 struct Walk {
   const PrefillParams* p;
   int TP;
-  int64_t u, u1, b;
+  int64_t u0, u1;      // the share
+  int64_t item, b;     // where the item starts; its sequence,
   Sequence s;
-  int pair, g, units;  // the item and its units
+  int pair, g, units;  // pair, KV head and units
   int j0, j1;          // this segment's units
+  __device__ __forceinline__ void cut() {
+    j0 = (int)max(u0 - item - kPfItemCost, (int64_t)0);
+    j1 = (int)min(max(u1 - item - kPfItemCost, (int64_t)0), (int64_t)units);
+  }
   __device__ __forceinline__ bool start(const PrefillParams& pp, const PfBarriers& sh, int TPT,
                                         int64_t begin, int64_t end) {
     p = &pp;
     TP = 2 * TPT;
-    u = begin;
+    u0 = begin;
     u1 = end;
-    if (u >= u1) return false;
+    if (u0 >= u1) return false;
     b = sh.plan.first_b;
     s = sequence(pp, b, TP);
     pair = sh.first_p;
     units = pair_units(s, pair, TP);
-    const int64_t local = u - sh.plan.first_prefix - pp.H_kv * units_before(s, pair, TP);
-    g = (int)(local / units);
-    j0 = (int)(local % units);
-    j1 = (int)min((int64_t)units, j0 + (u1 - u));
-    return true;
+    const int64_t pair0 = sh.plan.first_prefix + pp.H_kv * cost_before(s, pair, TP);
+    g = (int)((u0 - pair0) / (units + kPfItemCost));
+    item = pair0 + (int64_t)g * (units + kPfItemCost);
+    cut();
+    return j0 < j1 || next();
   }
   __device__ __forceinline__ bool next() {
-    u += j1 - j0;
-    if (u >= u1) return false;
-    if (++g == p->H_kv) {
-      g = 0;
-      if (++pair == s.pairs) {
-        pair = 0;
-        do s = sequence(*p, ++b, TP); while (s.pairs == 0);  // more units follow, so one has them
+    do {
+      item += units + kPfItemCost;
+      if (item >= u1) return false;
+      if (++g == p->H_kv) {
+        g = 0;
+        if (++pair == s.pairs) {
+          pair = 0;
+          do s = sequence(*p, ++b, TP); while (s.pairs == 0);  // more follow, so one has some
+        }
+        units = pair_units(s, pair, TP);
       }
-      units = pair_units(s, pair, TP);
-    }
-    j0 = 0;
-    j1 = (int)min((int64_t)units, u1 - u);
+      cut();
+    } while (j0 >= j1);
     return true;
   }
+  __device__ __forceinline__ bool last() const { return item + units + kPfItemCost >= u1; }
   // Tile t's tokens and the end of its units within this segment.
   __device__ __forceinline__ int first_token(int t) const { return pair * TP + t * (TP / 2); }
   __device__ __forceinline__ int tokens(int t) const {
@@ -310,7 +327,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
       [&](int64_t b, bool first) {
         const Sequence s = sequence(p, b, TP);
         if (first && s.bad && blockIdx.x == 0) atomicOr(p.ctl.status, kStatusBadInput);
-        return sequence_units(s, TP, p.H_kv);
+        return sequence_cost(s, TP, p.H_kv);
       },
       u0, u1);
   const int64_t total = sh.plan.total;
@@ -321,7 +338,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
       int lo = 0, hi = s.pairs;
       while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const bool le = at < hi && p.H_kv * units_before(s, at, TP) <= local;
+        const bool le = at < hi && p.H_kv * cost_before(s, at, TP) <= local;
         const int k = __popc(__ballot_sync(0xffffffffu, le));  // lane 0's holds: at least 1
         lo += (k - 1) * step;
         hi = min(hi, lo + step);
@@ -360,7 +377,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
         for (int j = w.j0; j < jend && ok; ++j) {
           for (int kv = 0; kv < 2; ++kv) {
             const int slot = nkv % p.slots;
-            if (p.ctl.drop_last && kv && j == jend - 1 && w.u + (w.j1 - w.j0) >= w.u1) {
+            if (p.ctl.drop_last && kv && j == jend - 1 && w.last()) {
               ok = false;  // testing: withhold the last tile
               break;
             }
@@ -587,8 +604,8 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
         ++no;
       }
       if (consumer_barrier_any<kTile>(1 + t, !ok)) break;
-      const int64_t item = w.u - w.j0;
-      const int cf = share_of(item, ctas, total), cl = share_of(item + w.units - 1, ctas, total);
+      const int64_t unit0 = w.item + kPfItemCost;  // the CTAs of the item's first and last unit
+      const int cf = share_of(unit0, ctas, total), cl = share_of(unit0 + w.units - 1, ctas, total);
       __nv_bfloat16* out =
           p.out + (((int64_t)w.s.c0 + first + tok_r) * p.H + (int64_t)w.g * p.G + head_r) * D;
       // this tile's part of a slot: m, l, then O as float4 [D / 4][rows]
