@@ -63,16 +63,21 @@ constexpr float kRescaleAbove = 8.f;
 // An item costs its units and, to start (Q, the first K) and to finish (O), about as
 // much as this many more; the shares of the CTAs are counted in both.
 #ifndef PF_ITEM
-#define PF_ITEM 3
+#define PF_ITEM 2
 #endif
 constexpr int kPfItemCost = PF_ITEM;
-// TMEM columns: S of the two tiles (W over the second half of each), O of the two tiles
-constexpr uint32_t kColS = 0, kColW = 64, kColO = 256, kPfTmemCols = 512;
+#ifndef PF_FMA
+#define PF_FMA 0
+#endif
+constexpr int kPfFma = PF_FMA;
+// TMEM columns: S of the two tiles in halves of 64 (W over the first 32 of each), O of them
+constexpr uint32_t kColS = 0, kColO = 256, kPfTmemCols = 512;
 
 struct PrefillParams {
   CUtensorMap q_map;   // [T][H_kv][G][D], box TPT x 1 x G x 64
   CUtensorMap k_map;   // [B H_kv][n_max][D], box 1 x 128 x 64
   CUtensorMap v_map;
+  CUtensorMap o_map;   // out, boxes as of q
   __nv_bfloat16* out;  // [T x H x D]
   const int32_t* cu;
   const int32_t* kv_len;
@@ -91,7 +96,7 @@ struct PrefillParams {
 struct PfBarriers {
   uint64_t q_full, q_empty;
   uint64_t kv_full[kPfMaxSlots], kv_empty[kPfMaxSlots];
-  uint64_t s_full[2], p_full[2], o_full[2], mma_done;
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], mma_done;  // [tile][half]
   uint32_t tmem;
   int abort, q_issued, kv_issued;
   int last[2];
@@ -208,6 +213,11 @@ struct Walk {
     } while (j0 >= j1);
     return true;
   }
+  // Halves (64 rows) that tile t sees of unit j < end_unit(t).
+  __device__ __forceinline__ int halves(int t, int j) const {
+    const int rows = s.len - s.n + first_token(t) + tokens(t) - j * kTile;
+    return rows > kTile / 2 ? 2 : 1;
+  }
   __device__ __forceinline__ bool last() const { return item + units + kPfItemCost >= u1; }
   // Tile t's tokens and the end of its units within this segment.
   __device__ __forceinline__ int first_token(int t) const { return pair * TP + t * (TP / 2); }
@@ -235,27 +245,34 @@ __device__ __forceinline__ void tma_load_q(void* dst, const void* tmap, int x, i
       ::"r"(smem_u32(dst)), "l"(tmap), "r"(x), "r"(0), "r"(g), "r"(t), "r"(smem_u32(bar)) : "memory");
 }
 
-// V tile as the B operand: element (k = row, n = column) of row-major rows of
-// 64 columns (128 bytes, swizzled): groups of 8 rows 1024 bytes apart, blocks of
-// 64 columns kPfBlock apart.
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(kPfBlock >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Operand descriptors, as their constant upper and address-bearing lower words: an
+// operand further on is one addition to the lower word (16-byte units), so that the
+// issuing thread keeps ahead of the tensor cores (building each descriptor anew took
+// longer than its product).  V as the B operand: element (k = row, n = column) of
+// row-major rows of 64 columns (128 bytes, swizzled), groups of 8 rows 1024 bytes
+// apart, blocks of 64 columns kPfBlock apart.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_v(uint32_t saddr) {
+  return (saddr >> 4) | ((uint32_t)(kPfBlock >> 4) << 16);
 }
 constexpr uint32_t kTransposeB = 1u << 16;
 
-// D (TMEM) += A (bf16 in TMEM) B (shared memory)
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                            uint32_t idesc, uint32_t accumulate) {
+// D (TMEM) = A B^T or += it: A and B in shared memory, or A as bf16 in TMEM.
+template <bool kAccumulate>
+__device__ __forceinline__ void pf_mma(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "n"(kDescHi), "r"(idesc), "n"((int)kAccumulate));
+}
+__device__ __forceinline__ void pf_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -285,6 +302,61 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return w;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 2^x of a pair on the FMA pipes, for -120 <= x (smaller ones give 2^-120): adding
+// 1.5 * 2^23 rounds x to an integer n, a cubic (fitted for the least largest relative
+// error over [-1/2, 1/2], 7.5e-5, against the 2^-9 of the rounding to bf16 that follows)
+// gives 2^(x - n), and n goes into the exponent bits.
+__device__ __forceinline__ void ex2_fma(float& x, float& y) {
+  constexpr float kMagic = 12582912.f;
+  const uint64_t v = pk2(fmaxf(x, -120.f), fmaxf(y, -120.f));
+  const uint64_t t = fadd2(v, pk2(kMagic, kMagic));
+  const uint64_t f = ffma2(fadd2(t, pk2(-kMagic, -kMagic)), pk2(-1.f, -1.f), v);
+  uint64_t q = ffma2(pk2(0.05517167f, 0.05517167f), f, pk2(0.24261113f, 0.24261113f));
+  q = ffma2(q, f, pk2(0.69326099f, 0.69326099f));
+  q = ffma2(q, f, pk2(0.99992807f, 0.99992807f));
+  float n0, n1, q0, q1;
+  unpk2(t, n0, n1);
+  unpk2(q, q0, q1);
+  x = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(n0) << 23));
+  y = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(n1) << 23));
+}
+// s[0..63] <- w = 2^(s sc + nref) as 32 bf16 pairs in s[0..31]; sum += w.  kFma of every
+// eight pairs take the FMA pipes, the others the exp2 unit.
+template <int kFma>
+__device__ __forceinline__ void weights(uint32_t (&s)[64], uint64_t sc2, uint64_t nref2,
+                                        uint64_t (&sum)[2]) {
+#pragma unroll
+  for (int i = 0; i < 64; i += 2) {
+    float x, y;
+    unpk2(ffma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, nref2), x, y);
+    if ((i >> 1) % 8 < kFma) {
+      ex2_fma(x, y);
+    } else {
+      x = ex2(x);
+      y = ex2(y);
+    }
+    sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], pk2(x, y));
+    s[i >> 1] = bf16x2(x, y);
+  }
+}
+
+__device__ __forceinline__ void tma_store_out(const void* tmap, const void* src, int x, int g, int t) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+          tmap),
+      "r"(x), "r"(0), "r"(g), "r"(t), "r"(smem_u32(src))
+      : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_read_wait() {  // the source may be written again
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1)
 attn_prefill(const __grid_constant__ PrefillParams p) {
@@ -294,9 +366,10 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   PfBarriers& sh = *reinterpret_cast<PfBarriers*>(smem);
   uint8_t* q_smem = smem + kPfHeader;
-  uint8_t* kv_smem = q_smem + 2 * kTileBytes;
+  uint8_t* o_smem = q_smem + 2 * kTileBytes;         // 64 columns of each tile's output
+  uint8_t* kv_smem = o_smem + 2 * kPfBlock;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int TPT = kTile / p.G, TP = 2 * TPT;
 
   if (threadIdx.x == 0) {
@@ -307,8 +380,11 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
       mbar_init(&sh.kv_empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.p_full[t], kTile);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sh.s_full[t][h], 1);
+        mbar_init(&sh.p_full[t][h], kTile);
+      }
+      mbar_init(&sh.pv_done[t], 1);
       mbar_init(&sh.o_full[t], 1);
     }
     mbar_init(&sh.mma_done, 1);
@@ -402,95 +478,93 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
     __syncwarp();
   } else if (warp == kPfMma) {
     // ---------------- MMA issuer ----------------
-    Walk w;
-    int nq = 0, nkv = 0;       // Q loads and K/V tiles consumed
-    int np[2] = {0, 0};        // W tiles consumed
-    bool ok = true;
-    constexpr uint32_t kIdescS = idesc_bf16(kTile), kIdescO = idesc_bf16(D) | kTransposeB;
-    const uint32_t q_addr = smem_u32(q_smem), kv_addr = smem_u32(kv_smem);
-    const auto wait = [&](uint64_t* bar, int phase) {
-      if (mbar_wait_warp(bar, (uint32_t)(phase & 1), wait_ns, abort)) return true;
-      if (lane == 0) {
+    if (elect_one()) {
+      Walk w;
+      int nq = 0, nkv = 0;              // Q loads and K/V tiles consumed
+      int np[2][2] = {{0, 0}, {0, 0}};  // W halves consumed
+      bool ok = true;
+      constexpr uint32_t kIdescS = idesc_bf16(kTile / 2), kIdescO = idesc_bf16(D) | kTransposeB;
+      const uint32_t q_lo = desc_k_major(smem_u32(q_smem)), kv_addr = smem_u32(kv_smem);
+      const auto wait = [&](uint64_t* bar, int phase) {
+        if (mbar_wait_bounded(bar, (uint32_t)(phase & 1), wait_ns, abort)) return true;
         sh.abort = 1;
         atomicOr(p.ctl.status, kStatusTimeout);
-      }
-      return false;
-    };
-    const auto qk = [&](int t, int slot) {  // S_t = Q_t K^T
-      if (lane == 0) {
-        const uint32_t a = q_addr + t * kTileBytes, b = kv_addr + slot * kTileBytes;
+        return false;
+      };
+      const auto qk = [&](int t, int h, int slot) {  // half h of S_t = Q_t K^T
+        const uint32_t a = q_lo + t * (kTileBytes >> 4);
+        const uint32_t b = desc_k_major(kv_addr + slot * kTileBytes + h * (kPfBlock / 2));
+        const uint32_t d = tmem + kColS + t * kTile + h * 64;
+        pf_mma<false>(d, a, b, kIdescS);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * kPfBlock + (k % 4) * 32;
-          mma_bf16(tmem + kColS + t * kTile, sw128_desc(a + off), sw128_desc(b + off), kIdescS, k > 0);
+        for (int k = 1; k < D / 16; ++k) {
+          const uint32_t off = ((k / 4) * kPfBlock + (k % 4) * 32) >> 4;
+          pf_mma<true>(d, a + off, b + off, kIdescS);
         }
-        mma_commit(&sh.s_full[t]);
-      }
-      __syncwarp();
-    };
-    for (bool more = w.start(p, sh, TPT, u0, u1); more && ok; more = w.next()) {
-      const int end[2] = {w.end_unit(0), w.end_unit(1)};
-      const int jend = max(end[0], end[1]);
-      if (jend == w.j0) continue;
-      if (!wait(&sh.q_full, nq)) break;
-      ++nq;
-      // the tiles arrive K, V, K, V, ...
-      int k_slot = nkv % p.slots;
-      if (!wait(&sh.kv_full[k_slot], nkv / p.slots)) break;
-      ++nkv;
-      tc_fence_after();
-      for (int t = 0; t < 2; ++t)
-        if (end[t] > w.j0) qk(t, k_slot);
-      if (lane == 0) mma_commit(&sh.kv_empty[k_slot]);
-      for (int j = w.j0; j < jend && ok; ++j) {
-        const int v_slot = nkv % p.slots;
-        if (!(ok = wait(&sh.kv_full[v_slot], nkv / p.slots))) break;
+        mma_commit(&sh.s_full[t][h]);
+      };
+      for (bool more = w.start(p, sh, TPT, u0, u1); more && ok; more = w.next()) {
+        const int end[2] = {w.end_unit(0), w.end_unit(1)};
+        const int jend = max(end[0], end[1]);
+        if (jend == w.j0) continue;
+        if (!wait(&sh.q_full, nq)) break;
+        ++nq;
+        // the tiles arrive K, V, K, V, ...
+        int k_slot = nkv % p.slots;
+        if (!wait(&sh.kv_full[k_slot], nkv / p.slots)) break;
         ++nkv;
-        // rows past the sequence's end may hold anything (0 * NaN is NaN)
-        const int held = w.s.len - j * kTile;
-        if (held < kTile) {
-          uint4* rows = reinterpret_cast<uint4*>(kv_smem + v_slot * kTileBytes);
-          for (int z = 0; z < kBlocks; ++z)
-            for (int i = held * 8 + lane; i < kTile * 8; i += 32)
-              rows[z * (kPfBlock / 16) + i] = make_uint4(0, 0, 0, 0);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
-        const bool more_k = j + 1 < jend;
-        if (more_k) {
-          k_slot = nkv % p.slots;
-          if (!(ok = wait(&sh.kv_full[k_slot], nkv / p.slots))) break;
+        tc_fence_after();
+        int have[2] = {end[0] > w.j0 ? w.halves(0, w.j0) : 0, end[1] > w.j0 ? w.halves(1, w.j0) : 0};
+        for (int h = 0; h < 2; ++h)
+          for (int t = 0; t < 2; ++t)
+            if (h < have[t]) qk(t, h, k_slot);
+        mma_commit(&sh.kv_empty[k_slot]);
+        if (jend == w.j0 + 1) mma_commit(&sh.q_empty);  // Q has had its last product
+        for (int j = w.j0; j < jend; ++j) {
+          const int v_slot = nkv % p.slots;
+          if (!(ok = wait(&sh.kv_full[v_slot], nkv / p.slots))) break;
           ++nkv;
-        }
-        for (int t = 0; t < 2; ++t) {
-          if (j < end[t]) {
-            if (!(ok = wait(&sh.p_full[t], np[t]))) break;
-            ++np[t];
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t v = kv_addr + v_slot * kTileBytes;
+          const bool more_k = j + 1 < jend;
+          if (more_k) {
+            k_slot = nkv % p.slots;
+            if (!(ok = wait(&sh.kv_full[k_slot], nkv / p.slots))) break;
+            ++nkv;
+          }
+          const int next[2] = {j + 1 < end[0] ? w.halves(0, j + 1) : 0, j + 1 < end[1] ? w.halves(1, j + 1) : 0};
 #pragma unroll
-              for (int k = 0; k < kTile / 16; ++k)
-                mma_bf16_ta(tmem + kColO + t * kTile, tmem + kColS + kColW + t * kTile + k * 8,
-                            v_desc(v + k * 2048), kIdescO, j > w.j0 || k > 0);
-              if (j + 1 >= end[t]) mma_commit(&sh.o_full[t]);
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (h >= have[t] || !ok) continue;
+              if (!(ok = wait(&sh.p_full[t][h], np[t][h]))) continue;
+              ++np[t][h];
+              tc_fence_after();
+              const uint32_t v = desc_v(kv_addr + v_slot * kTileBytes + h * (kPfBlock / 2));
+              const uint32_t d = tmem + kColO + t * kTile;
+              const uint32_t a = tmem + kColS + t * kTile + h * 64;
+              pf_mma_ta(d, a, v, kIdescO, j > w.j0 || h > 0);
+#pragma unroll
+              for (int k = 1; k < 4; ++k)
+                pf_mma_ta(d, a + k * 8, v + k * (2048 >> 4), kIdescO, 1);
+              mma_commit(&sh.pv_done[t]);
+              if (j + 1 >= end[t] && h + 1 >= have[t]) mma_commit(&sh.o_full[t]);
+              if (h < next[t]) qk(t, h, k_slot);
             }
-            __syncwarp();
-            if (j + 1 < end[t]) qk(t, k_slot);
+          }
+          if (!ok) break;
+          have[0] = next[0];
+          have[1] = next[1];
+          mma_commit(&sh.kv_empty[v_slot]);
+          if (more_k) {
+            mma_commit(&sh.kv_empty[k_slot]);
+            if (j + 2 == jend) mma_commit(&sh.q_empty);
           }
         }
-        if (!ok) break;
-        if (lane == 0) {
-          mma_commit(&sh.kv_empty[v_slot]);
-          if (more_k) mma_commit(&sh.kv_empty[k_slot]);
-        }
       }
-      if (ok && lane == 0) mma_commit(&sh.q_empty);
-    }
-    __syncwarp();
-    if (sh.abort && lane == 0) {  // the MMAs in flight read shared memory and write TMEM
-      mma_commit(&sh.mma_done);
-      mbar_wait_bounded(&sh.mma_done, 0, kDrainNs, nullptr);
+      if (sh.abort) {  // MMAs in flight read shared memory and write TMEM
+        mma_commit(&sh.mma_done);
+        mbar_wait_bounded(&sh.mma_done, 0, kDrainNs, nullptr);
+      }
     }
     __syncwarp();
   } else {
@@ -501,9 +575,20 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
     const uint32_t o_addr = tmem + lane_base + kColO + t * kTile;
     const int tok_r = r / p.G, head_r = r % p.G;
     Walk w;
-    int ns = 0, no = 0;  // S and O tiles consumed
+    int ns[2] = {0, 0};  // halves of S consumed
+    int no = 0;          // finished O taken
+    int nu = 0;          // units of the CTA before this segment
+    const auto wait = [&](uint64_t* bar, int phase) {
+      if (mbar_wait_warp(bar, (uint32_t)(phase & 1), wait_ns, abort)) return true;
+      if (lane == 0) {
+        sh.abort = 1;
+        atomicOr(p.ctl.status, kStatusTimeout);
+      }
+      return false;
+    };
     for (bool more = w.start(p, sh, TPT, u0, u1); more; more = w.next()) {
-      const int ntok = w.tokens(t);
+      const int ntok = w.tokens(t), unit0 = nu;
+      nu += max(w.end_unit(0), w.end_unit(1)) - w.j0;
       if (ntok == 0) continue;
       const int jend = w.end_unit(t);
       const bool row_ok = tok_r < ntok && r < TPT * p.G;
@@ -513,99 +598,88 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
       const int rows = w.s.len - w.s.n + first + min(tok_r, ntok - 1) + 1;  // KV rows it sees
       float m = -CUDART_INF_F, l = 0.f;
       bool ok = true;
-      for (int j = w.j0; j < jend; ++j) {
-        if (!mbar_wait_warp(&sh.s_full[t], (uint32_t)(ns & 1), wait_ns, abort)) {
-          if (lane == 0) {
-            sh.abort = 1;
-            atomicOr(p.ctl.status, kStatusTimeout);
-          }
-          ok = false;
-          break;
+      for (int j = w.j0; j < jend && ok; ++j) {
+        const int held = w.s.len - j * kTile;
+        if (held < kTile) {
+          // V's rows past the sequence's end may hold anything, and 0 * NaN is NaN: zeroed
+          // before this tile's products (tiles arrive K, V, K, V, ..., by unit)
+          const int n = 2 * (unit0 + j - w.j0) + 1, slot = n % p.slots;
+          if (!(ok = wait(&sh.kv_full[slot], n / p.slots))) break;
+          uint4* v = reinterpret_cast<uint4*>(kv_smem + slot * kTileBytes);
+          for (int z = 0; z < kBlocks; ++z)
+            for (int i = held * 8 + r; i < kTile * 8; i += kTile)
+              v[z * (kPfBlock / 16) + i] = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        ++ns;
-        if (warp_ok) {
-          tc_fence_after();
-          // S in halves of 64 columns (128 would not fit the registers beside the rest):
-          // the maximum over both, then W of the second half, still held, then of the
-          // first, read again.  W lies over the second half of S.
-          uint32_t s[64];
-          const int cols = rows - j * kTile;
-          const bool cut = __any_sync(0xffffffffu, cols < kTile);
-          const auto load = [&](int c0) {
-            tmem_ld<32>(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-            tmem_ld<32>(s_addr + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+        const int halves = w.halves(t, j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h >= halves || !ok) continue;
+          if (!(ok = wait(&sh.s_full[t][h], ns[h]))) continue;
+          ++ns[h];
+          if (warp_ok) {
+            tc_fence_after();
+            uint32_t s[64];
+            tmem_ld<32>(s_addr + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld<32>(s_addr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
             tmem_wait();
+            const int cols = rows - j * kTile - h * 64;
+            const bool cut = __any_sync(0xffffffffu, cols < 64);
             if (cut) {
 #pragma unroll
               for (int i = 0; i < 64; ++i)
-                if (c0 + i >= cols) s[i] = 0xff800000u;  // -inf
+                if (i >= cols) s[i] = 0xff800000u;  // -inf
             }
-          };
-          float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            load(half * 64);
+            float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
             for (int i = 0; i < 64; i += 8)
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(s[i + 2 * c]), __uint_as_float(s[i + 2 * c + 1])));
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-          if (j == w.j0) {
-            m = top;
-          } else if (__any_sync(0xffffffffu, top > m + kRescaleAbove)) {
-            const float mnew = fmaxf(m, top);
-            const float f = mnew == m ? 1.f : ex2(m - mnew);
-            m = mnew;
-            l *= f;
+                mx[c] = max3(mx[c], __uint_as_float(s[i + 2 * c]), __uint_as_float(s[i + 2 * c + 1]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+            if (j == w.j0 && h == 0) {
+              m = top;
+            } else if (__any_sync(0xffffffffu, top > m + kRescaleAbove)) {
+              // this S came after the product with W of two halves ago, so only the last
+              // one's can be pending (the phase waited for is the barrier's or the one before)
+              if (!(ok = wait(&sh.pv_done[t], ns[0] + ns[1] - 2))) continue;
+              tc_fence_after();
+              const float mnew = fmaxf(m, top);
+              const float f = mnew == m ? 1.f : ex2(m - mnew);
+              m = mnew;
+              l *= f;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld<32>(o_addr + c * 32, o);
-              tmem_wait();
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld<32>(o_addr + c * 32, o);
+                tmem_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(o_addr + c * 32, o);
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(o_addr + c * 32, o);
+              }
             }
+            const float ref = m == -CUDART_INF_F ? 0.f : m;
+            const uint64_t sc2 = pk2(p.scale_log2, p.scale_log2), ref2 = pk2(-ref, -ref);
+            uint64_t sum[2] = {0ull, 0ull};
+            if (cut)
+              weights<0>(s, sc2, ref2, sum);  // masked scores give exact zeros
+            else
+              weights<kPfFma>(s, sc2, ref2, sum);
+            tmem_st32(s_addr + h * 64, s);
+            l += hsum2(fadd2(sum[0], sum[1]));
+            tmem_st_wait();
+            tc_fence_before();
           }
-          const float ref = m == -CUDART_INF_F ? 0.f : m;
-          const uint64_t sc2 = pk2(p.scale_log2, p.scale_log2), ref2 = pk2(-ref, -ref);
-          uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-          for (int half = 1; half >= 0; --half) {
-            if (half == 0) load(0);
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              float x, y;
-              unpk2(ffma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, ref2), x, y);
-              x = ex2(x);
-              y = ex2(y);
-              sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], pk2(x, y));
-              s[i >> 1] = bf16x2(x, y);
-            }
-            tmem_st32(s_addr + kColW + half * 32, s);
-          }
-          l += hsum2(fadd2(sum[0], sum[1]));
-          tmem_st_wait();
-          tc_fence_before();
+          mbar_arrive(&sh.p_full[t][h]);
         }
-        mbar_arrive(&sh.p_full[t]);
       }
       const bool any = jend > w.j0;
       if (ok && any) {
-        if (!mbar_wait_warp(&sh.o_full[t], (uint32_t)(no & 1), wait_ns, abort)) {
-          if (lane == 0) {
-            sh.abort = 1;
-            atomicOr(p.ctl.status, kStatusTimeout);
-          }
-          ok = false;
-        }
-        ++no;
+        ok = wait(&sh.o_full[t], no++);
       }
       if (consumer_barrier_any<kTile>(1 + t, !ok)) break;
-      const int64_t unit0 = w.item + kPfItemCost;  // the CTAs of the item's first and last unit
-      const int cf = share_of(unit0, ctas, total), cl = share_of(unit0 + w.units - 1, ctas, total);
+      const int64_t begin = w.item + kPfItemCost;  // the CTAs of the item's first and last unit
+      const int cf = share_of(begin, ctas, total), cl = share_of(begin + w.units - 1, ctas, total);
       __nv_bfloat16* out =
           p.out + (((int64_t)w.s.c0 + first + tok_r) * p.H + (int64_t)w.g * p.G + head_r) * D;
       // this tile's part of a slot: m, l, then O as float4 [D / 4][rows]
@@ -613,46 +687,69 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
         const int slot = c == cf ? 2 * c + 1 : 2 * c;
         return p.partials + ((size_t)slot * p.piece_tiles + t) * p.piece_rows * (2 + D);
       };
-      if (warp_ok) {
-        tc_fence_after();
-        const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+      const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+      const auto load_o = [&](int c, uint32_t (&o)[32]) {  // columns c .. c + 31
+        if (any) {
+          tmem_ld<32>(o_addr + c, o);
+          tmem_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+      };
+      const auto pack8 = [&](const uint32_t* o) {
+        return make_uint4(bf16x2(__uint_as_float(o[0]) * inv, __uint_as_float(o[1]) * inv),
+                          bf16x2(__uint_as_float(o[2]) * inv, __uint_as_float(o[3]) * inv),
+                          bf16x2(__uint_as_float(o[4]) * inv, __uint_as_float(o[5]) * inv),
+                          bf16x2(__uint_as_float(o[6]) * inv, __uint_as_float(o[7]) * inv));
+      };
+      tc_fence_after();
+      if (cf == cl && ntok == TPT) {
+        // a whole tile: through shared memory, 64 columns at a time, and one TMA store
+        // (a thread's own row in 16-byte stores would touch 32 lines an instruction)
+        uint8_t* stage = o_smem + t * kPfBlock;
+#pragma unroll
+        for (int z = 0; z < kBlocks; ++z) {
+          if (r == 0) tma_store_read_wait();  // of the stage's last contents
+          named_barrier_sync(1 + t, kTile);
+#pragma unroll
+          for (int c = 0; c < 64 && z * 64 + c < D; c += 32) {
+            uint32_t o[32];
+            load_o(z * 64 + c, o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(stage + r * 128 + (((c / 8 + i) ^ (r & 7)) << 4)) =
+                  pack8(o + 8 * i);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          named_barrier_sync(1 + t, kTile);
+          if (r == 0) tma_store_out(&p.o_map, stage, z * 64, w.g, w.s.c0 + first);
+        }
+      } else if (warp_ok) {
         float* pc = piece((int)blockIdx.x);
         if (cf != cl && row_ok) {
           pc[r] = m;
           pc[p.piece_rows + r] = l;
         }
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
-          if (any) {
-            tmem_ld<32>(o_addr + c * 32, o);
-            tmem_wait();
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0;
-          }
+          load_o(c, o);
           if (!row_ok) continue;
           if (cf == cl) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint4 v;
-              v.x = bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-              v.y = bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-              v.z = bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-              v.w = bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
-              *reinterpret_cast<uint4*>(out + c * 32 + i) = v;
-            }
+            for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(out + c + i) = pack8(o + i);
           } else {
             float4* dst = reinterpret_cast<float4*>(pc + 2 * p.piece_rows);
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              dst[(c * 8 + i / 4) * p.piece_rows + r] =
+              dst[(c + i) / 4 * p.piece_rows + r] =
                   make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
                               __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
           }
         }
-        tc_fence_before();
       }
+      tc_fence_before();
       if (cf != cl) {
         __threadfence();
         named_barrier_sync(1 + t, kTile);
@@ -671,23 +768,30 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
               L = fmaf(exp2f(__ldcg(piece(c) + r) - M), __ldcg(piece(c) + p.piece_rows + r), L);
             const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
 #pragma unroll 1
-            for (int d8 = 0; d8 < D / 8; ++d8) {
-              float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+            for (int d0 = 0; d0 < D; d0 += 32) {  // 8 loads of a piece in flight
+              float acc[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[i] = 0.f;
               for (int c = cf; c <= cl; ++c) {
                 const float* pc = piece(c);
+                const float4* src = reinterpret_cast<const float4*>(pc + 2 * p.piece_rows) + (size_t)(d0 / 4) * p.piece_rows + r;
+                float4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + i * p.piece_rows);
                 const float f = exp2f(__ldcg(pc + r) - M);
-                const float4* src = reinterpret_cast<const float4*>(pc + 2 * p.piece_rows);
-                const float4 a = __ldcg(src + (2 * d8) * p.piece_rows + r);
-                const float4 b = __ldcg(src + (2 * d8 + 1) * p.piece_rows + r);
-                acc[0] = fmaf(f, a.x, acc[0]); acc[1] = fmaf(f, a.y, acc[1]);
-                acc[2] = fmaf(f, a.z, acc[2]); acc[3] = fmaf(f, a.w, acc[3]);
-                acc[4] = fmaf(f, b.x, acc[4]); acc[5] = fmaf(f, b.y, acc[5]);
-                acc[6] = fmaf(f, b.z, acc[6]); acc[7] = fmaf(f, b.w, acc[7]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  acc[4 * i] = fmaf(f, v[i].x, acc[4 * i]);
+                  acc[4 * i + 1] = fmaf(f, v[i].y, acc[4 * i + 1]);
+                  acc[4 * i + 2] = fmaf(f, v[i].z, acc[4 * i + 2]);
+                  acc[4 * i + 3] = fmaf(f, v[i].w, acc[4 * i + 3]);
+                }
               }
-              *reinterpret_cast<uint4*>(out + d8 * 8) =
-                  make_uint4(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv),
-                             bf16x2(acc[4] * inv, acc[5] * inv), bf16x2(acc[6] * inv, acc[7] * inv));
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(out + d0 + i) =
+                    make_uint4(bf16x2(acc[i] * inv, acc[i + 1] * inv), bf16x2(acc[i + 2] * inv, acc[i + 3] * inv),
+                               bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), bf16x2(acc[i + 6] * inv, acc[i + 7] * inv));
             }
           }
           if (r == 0) atomicExch(p.counters + 2 * cf + t, 0u);
@@ -695,6 +799,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
         named_barrier_sync(1 + t, kTile);  // sh.last is written again
       }
     }
+    if (r == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncthreads();
   if (threadIdx.x == 0 && sh.abort) {  // copies in flight land in this CTA's memory
@@ -728,7 +833,7 @@ cudaError_t launch_prefill_d(PrefillParams& p, const DeviceInfo& dev, cudaStream
       done.insert(dev.device);
     }
   }
-  const size_t fixed = 1024 + kPfHeader + 2 * kTileBytes;  // alignment, barriers, Q
+  const size_t fixed = 1024 + kPfHeader + 2 * kTileBytes + 2 * kPfBlock;  // alignment, barriers, Q, out
   p.slots = (int)std::min<size_t>(kPfMaxSlots, (dev.max_smem_optin - fixed) / kTileBytes);
   if (p.slots < 4) return cudaErrorInvalidValue;  // a V, the next K and one of each ahead
   cudaLaunchConfig_t cfg = {};
@@ -796,6 +901,8 @@ cudaError_t launch_attn_prefill(const void* q, int64_t q_stride, const void* k_c
   const uint64_t q_strides[3] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2, (uint64_t)q_stride * 2};
   const uint32_t q_box[4] = {64, (uint32_t)p.G, 1, (uint32_t)(kTile / p.G)};
   cudaError_t e = encode_tmap_bf16(&p.q_map, q, 4, q_dims, q_strides, q_box);
+  const uint64_t o_strides[3] = {q_strides[0], q_strides[1], (uint64_t)H * D * 2};
+  if (e == cudaSuccess) e = encode_tmap_bf16(&p.o_map, out, 4, q_dims, o_strides, q_box);
   const uint64_t dims[3] = {(uint64_t)D, (uint64_t)n_max, (uint64_t)(B * H_kv)};
   const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)n_max * D * 2};
   const uint32_t box[3] = {64, kTile, 1};

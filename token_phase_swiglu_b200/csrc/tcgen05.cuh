@@ -99,6 +99,17 @@ __device__ __forceinline__ void tmem_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// One lane of a converged warp.  The issuer of tcgen05.mma is picked this way: the
+// compiler knows that a single lane is behind the branch and keeps the operands in
+// uniform registers.  Behind `lane == 0` it moves them there for every product: a group
+// of 8 after a barrier wait takes 640 cycles instead of 519 (128 columns wide, 64 cycles
+// each to execute) or 390 (64 wide).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // Barrier of the four epilogue warps that also ORs a failure flag, so that a
 // timeout in any of them makes all of them leave together.
 __device__ __forceinline__ bool epilogue_barrier_any(bool failed) {
