@@ -50,6 +50,12 @@ constexpr int kQ8TileBytes = kU * 128;
 constexpr int kQ8SlotBytes = 2 * kQ8TileBytes + 1024;  // K, V, then both rows of scales
 constexpr int kQ8Header = 1024;
 constexpr int kQ8MaxCtas = 256;
+// A region costs its units and, to start and to finish, about as much as this many
+// more; the shares of the CTAs are counted in both.
+#ifndef Q8_REGION
+#define Q8_REGION 4
+#endif
+constexpr int kRegionCost = Q8_REGION;
 
 struct Q8Params {
   CUtensorMap k_map, v_map;  // int8 [B H_kv][n_max][D], box 1 x 128 x 128
@@ -93,12 +99,17 @@ __device__ __forceinline__ uint32_t idesc_i8(int N) {  // int8 x int8 -> int32, 
   return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kU >> 4) << 24);
 }
 constexpr uint32_t kTransposeA = 1u << 15;
-__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+// Operand tiles have rows of 128 bytes with the 128-byte swizzle, groups of 8 rows 1024
+// bytes apart; a descriptor is this constant upper word and a lower one with the address.
+constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t operand(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::i8 [%0], a, b, %4, p;\n}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "n"(kOperandHi), "r"(idesc), "n"((int)kAccumulate));
 }
 __device__ __forceinline__ void tma_load_rows(void* dst, const void* tmap, int y, int z, uint64_t* bar,
                                               uint64_t policy) {
@@ -154,43 +165,50 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[N]) {
 // A (sequence, KV head) region's units; an empty one still takes one (its zeros).
 __device__ __forceinline__ int region_units(int len) { return max((len + kU - 1) / kU, 1); }
 
-// Walks the segments (parts of regions) of a CTA's unit range.
+// Walks the segments (parts of regions) of a CTA's share.  Unit j of a region stands at
+// cost kRegionCost + j behind its start, so a share may hold a region's start and none of
+// its units: such segments are passed over.
 struct Q8Walk {
   const Q8Params* p;
-  int64_t u, u1, b;
+  int64_t u0, u1, region, b;  // the share; where the region starts, its sequence
   int g, len, units, j0, j1;
   __device__ __forceinline__ void load() {
     len = __ldg(p->kv_len + b);
     units = region_units(len);
   }
+  __device__ __forceinline__ void cut() {
+    j0 = (int)max(u0 - region - kRegionCost, (int64_t)0);
+    j1 = (int)min(max(u1 - region - kRegionCost, (int64_t)0), (int64_t)units);
+  }
   template <typename Plan>
   __device__ __forceinline__ bool start(const Q8Params& pp, const Plan& plan, int64_t begin, int64_t end) {
     p = &pp;
-    u = begin;
+    u0 = begin;
     u1 = end;
-    if (u >= u1) return false;
+    if (u0 >= u1) return false;
     b = plan.first_b;
     load();
-    const int64_t local = u - plan.first_prefix;
-    g = (int)(local / units);
-    j0 = (int)(local % units);
-    j1 = (int)min((int64_t)units, j0 + (u1 - u));
-    return true;
+    g = (int)((u0 - plan.first_prefix) / (units + kRegionCost));
+    region = plan.first_prefix + (int64_t)g * (units + kRegionCost);
+    cut();
+    return j0 < j1 || next();
   }
   __device__ __forceinline__ bool next() {
-    u += j1 - j0;
-    if (u >= u1) return false;
-    if (++g == p->H_kv) {
-      g = 0;
-      do {
-        ++b;
-        load();
-      } while (len < 0 || len > p->n_max);  // more units follow, so one is taken
-    }
-    j0 = 0;
-    j1 = (int)min((int64_t)units, u1 - u);
+    do {
+      region += units + kRegionCost;
+      if (region >= u1) return false;
+      if (++g == p->H_kv) {
+        g = 0;
+        do {
+          ++b;
+          load();
+        } while (len < 0 || len > p->n_max);  // more follow, so one is taken
+      }
+      cut();
+    } while (j0 >= j1);
     return true;
   }
+  __device__ __forceinline__ bool last() const { return region + units + kRegionCost >= u1; }
   __device__ __forceinline__ int count() const { return len ? j1 - j0 : 0; }  // units with rows
 };
 
@@ -207,7 +225,7 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
   static_assert(sizeof(Q8Shared<GP>) <= kQ8Header, "header");
   static_assert(q8_cols(GP) * 128 % 1024 == 0, "operand tiles are whole swizzle atoms");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.slots; ++i) {
       mbar_init(&sh.full[i], 1 + 32);
@@ -243,7 +261,7 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
           if (first && blockIdx.x == 0) atomicOr(p.ctl.status, kStatusBadInput);
           return 0;
         }
-        return (int64_t)p.H_kv * region_units(len);
+        return (int64_t)p.H_kv * (region_units(len) + kRegionCost);
       },
       u0, u1);
   const int64_t total = sh.plan.total;
@@ -269,7 +287,7 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
       const int n = w.count();
       for (int i = 0; i < n; ++i, ++k) {
         const int slot = k % p.slots, row0 = (w.j0 + i) * kU;
-        if (p.ctl.drop_last && i == n - 1 && w.u + (w.j1 - w.j0) >= w.u1) {  // testing
+        if (p.ctl.drop_last && i == n - 1 && w.last()) {  // testing
           ok = false;
           break;
         }
@@ -327,60 +345,62 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
     }
     __syncwarp();
   } else if (warp == kQ8Mma) {
-    // ---------------- MMA issuer ----------------
-    Q8Walk w;
-    const uint32_t idesc = idesc_i8(N);
-    const uint32_t ring_addr = smem_u32(ring);
-    int kq = 0, s = 0, i = 0;  // S products issued; segment and unit of the next one
-    bool ok = true, more = w.start(p, sh.plan, u0, u1);
-    while (more && w.count() == 0) more = w.next();
-    const auto next_qk = [&]() {  // S^T of unit kq
-      if (!more) return;
-      if (i == 0 && !(ok = wait(&sh.q_full[s & 1], s / 2))) return;
-      const int slot = kq % p.slots;
-      if (!(ok = wait(&sh.full[slot], kq / p.slots))) return;
-      tc_fence_after();
-      const bool last = i + 1 == w.count();
-      if (lane == 0) {
-        // the scales came through cp.async, the tiles through the async proxy
-        const uint32_t a = ring_addr + slot * kQ8SlotBytes, b = smem_u32(tl.q[s & 1]);
+    // ---------------- MMA issuer (one lane) ----------------
+    if (elect_one()) {
+      Q8Walk w;
+      const uint32_t idesc = idesc_i8(N);
+      const uint32_t ring_lo = operand(smem_u32(ring));
+      const uint32_t q_lo[2] = {operand(smem_u32(tl.q[0])), operand(smem_u32(tl.q[1]))};
+      const uint32_t w_lo[2] = {operand(smem_u32(tl.w[0])), operand(smem_u32(tl.w[1]))};
+      const auto wait_one = [&](uint64_t* bar, int phase) {
+        if (mbar_wait_bounded(bar, (uint32_t)(phase & 1), p.ctl.wait_ns, abort)) return true;
+        sh.abort = 1;
+        atomicOr(p.ctl.status, kStatusTimeout);
+        return false;
+      };
+      int kq = 0, s = 0, i = 0;  // S products issued; segment and unit of the next one
+      bool ok = true, more = w.start(p, sh.plan, u0, u1);
+      while (more && w.count() == 0) more = w.next();
+      const auto next_qk = [&]() {  // S^T of unit kq
+        if (!more) return;
+        if (i == 0 && !(ok = wait_one(&sh.q_full[s & 1], s / 2))) return;
+        const int slot = kq % p.slots;
+        if (!(ok = wait_one(&sh.full[slot], kq / p.slots))) return;
+        tc_fence_after();
+        const bool last = i + 1 == w.count();
+        const uint32_t a = ring_lo + slot * (kQ8SlotBytes >> 4), b = q_lo[s & 1], d = tmem + (kq & 1) * N;
+        mma_i8<false>(d, a, b, idesc);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-          mma_i8(tmem + (kq & 1) * N, sw128_desc(a + c * 32), sw128_desc(b + c * 32), idesc, c > 0);
+        for (int c = 1; c < D / 32; ++c) mma_i8<true>(d, a + c * 2, b + c * 2, idesc);
         mma_commit(&sh.s_full[kq & 1]);
         if (last) mma_commit(&sh.q_empty[s & 1]);
-      }
-      __syncwarp();
-      ++kq;
-      ++i;
-      if (last) {
-        ++s;
-        i = 0;
-        do more = w.next(); while (more && w.count() == 0);
-      }
-    };
-    next_qk();
-    if (ok) next_qk();
-    for (int k = 0; ok && k < kq; ++k) {
-      const int wg = k & 1, slot = k % p.slots;
-      if (!(ok = wait(&sh.p_full[wg], k >> 1))) break;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t a = ring_addr + slot * kQ8SlotBytes + kQ8TileBytes, b = smem_u32(tl.w[wg]);
+        ++kq;
+        ++i;
+        if (last) {
+          ++s;
+          i = 0;
+          do more = w.next(); while (more && w.count() == 0);
+        }
+      };
+      next_qk();
+      if (ok) next_qk();
+      for (int k = 0; ok && k < kq; ++k) {
+        const int wg = k & 1, slot = k % p.slots;
+        if (!(ok = wait_one(&sh.p_full[wg], k >> 1))) break;
+        tc_fence_after();
+        const uint32_t a = ring_lo + slot * (kQ8SlotBytes >> 4) + (kQ8TileBytes >> 4), b = w_lo[wg];
+        const uint32_t d = tmem + (2 + wg) * N;
+        mma_i8<false>(d, a, b, idesc | kTransposeA);
 #pragma unroll
-        for (int c = 0; c < kU / 32; ++c)
-          mma_i8(tmem + (2 + wg) * N, sw128_desc(a + c * 4096), sw128_desc(b + c * 32),
-                 idesc | kTransposeA, c > 0);
+        for (int c = 1; c < kU / 32; ++c) mma_i8<true>(d, a + c * (4096 >> 4), b + c * 2, idesc | kTransposeA);
         mma_commit(&sh.o_full[wg]);
         mma_commit(&sh.empty[slot]);
+        next_qk();  // W of unit k is in, so its S has been read
       }
-      __syncwarp();
-      next_qk();  // W of unit k is in, so its S has been read
-    }
-    __syncwarp();
-    if (sh.abort && lane == 0) {
-      mma_commit(&sh.mma_done);
-      mbar_wait_bounded(&sh.mma_done, 0, kDrainNs, nullptr);
+      if (sh.abort) {
+        mma_commit(&sh.mma_done);
+        mbar_wait_bounded(&sh.mma_done, 0, kDrainNs, nullptr);
+      }
     }
     __syncwarp();
   } else {
@@ -487,13 +507,13 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
         }
       }
       if (consumer_barrier_any<2 * kU>(1, !ok)) break;
+      const int64_t begin = w.region + kRegionCost;  // the CTAs of the region's first and last unit
+      const int cf = share_of(begin, ctas, total), cl = share_of(begin + w.units - 1, ctas, total);
+      float* out = p.out + (w.b * p.H + (int64_t)w.g * p.G) * D;
+      const auto piece = [&](int c, int h) {
+        return p.partials + ((size_t)(c == cf ? 2 * c + 1 : 2 * c) * p.G + h) * (3 + D);
+      };
       if (wg == 0) {
-        const int64_t region = w.u - w.j0;
-        const int cf = share_of(region, ctas, total), cl = share_of(region + w.units - 1, ctas, total);
-        float* out = p.out + (w.b * p.H + (int64_t)w.g * p.G) * D;
-        const auto piece = [&](int c, int h) {
-          return p.partials + ((size_t)(c == cf ? 2 * c + 1 : 2 * c) * p.G + h) * (3 + D);
-        };
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
           if (h >= p.G) break;
@@ -512,32 +532,48 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
             if (r < D) pc[3 + r] = A;
           }
         }
-        if (cf != cl) {
+      }
+      if (cf != cl) {
+        if (wg == 0) {
           __threadfence();
           named_barrier_sync(2, kU);
           if (r == 0) sh.last = atomicAdd(p.counters + cf, 1u) == (uint32_t)(cl - cf);
-          named_barrier_sync(2, kU);
-          if (sh.last) {
-            __threadfence();
-            for (int h = 0; h < p.G; ++h) {
-              float M = -CUDART_INF_F, R = -CUDART_INF_F, L = 0.f, A = 0.f;
-#pragma unroll 4
-              for (int c = cf; c <= cl; ++c) {
-                M = fmaxf(M, __ldcg(piece(c, h)));
-                R = fmaxf(R, __ldcg(piece(c, h) + 2));
+        }
+        named_barrier_sync(1, 2 * kU);
+        if (sh.last) {  // a warp per head; a lane per piece, then per column
+          __threadfence();
+          for (int h = warp; h < p.G; h += 8) {
+            float M = -CUDART_INF_F, R = -CUDART_INF_F, L = 0.f, A[D / 32];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) A[i] = 0.f;
+            for (int c = cf + lane; c <= cl; c += 32) {
+              M = fmaxf(M, __ldcg(piece(c, h)));
+              R = fmaxf(R, __ldcg(piece(c, h) + 2));
+            }
+            M = warp_top(M);
+            R = warp_top(R);
+            for (int c0 = cf; c0 <= cl; c0 += 32) {
+              float f = 0.f;
+              if (c0 + lane <= cl) {
+                const float* pc = piece(c0 + lane, h);
+                L = fmaf(__ldcg(pc + 1), ex2_diff(__ldcg(pc), M), L);
+                f = ex2_diff(__ldcg(pc + 2), R);
               }
-              if (r < D) {
+              const int n = min(32, cl - c0 + 1);
 #pragma unroll 4
-                for (int c = cf; c <= cl; ++c) {
-                  const float* pc = piece(c, h);
-                  L = fmaf(__ldcg(pc + 1), ex2_diff(__ldcg(pc), M), L);
-                  A = fmaf(__ldcg(pc + 3 + r), ex2_diff(__ldcg(pc + 2), R), A);
-                }
-                out[h * D + r] = L == 0.f ? 0.f : A * ex2_diff(R, M) / (127.f * L);
+              for (int k = 0; k < n; ++k) {
+                const float* pc = piece(c0 + k, h) + 3 + lane;
+                const float fk = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) A[i] = fmaf(__ldcg(pc + 32 * i), fk, A[i]);
               }
             }
-            if (r == 0) atomicExch(p.counters + cf, 0u);
+            L = warp_sum(L);
+            const float s = L == 0.f ? 0.f : ex2_diff(R, M) / (127.f * L);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) out[h * D + lane + 32 * i] = A[i] * s;
           }
+          if (threadIdx.x == 0) atomicExch(p.counters + cf, 0u);
         }
       }
       if (consumer_barrier_any<2 * kU>(1, false)) break;  // what was exchanged is written again

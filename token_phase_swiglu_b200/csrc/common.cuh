@@ -109,10 +109,19 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     if (globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
-// The same by a whole warp, all of whose lanes get the same answer.
+// The same by a whole warp, all of whose lanes get the same answer.  It sleeps between
+// the tests: several warps testing without a pause take issue slots and shared-memory
+// cycles from the warps they wait for.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
                                                volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit_ns, abort));
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    __nanosleep(64);
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    const bool give_up = (abort && *abort) || globaltimer_ns() - t0 > limit_ns;
+    if (__any_sync(0xffffffffu, give_up)) return false;
+  }
 }
 // Bulk copy global -> shared of `bytes` (16-byte aligned both sides, bytes % 16
 // == 0); completion is counted as transaction bytes on `bar`.
