@@ -136,8 +136,15 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's handle without the Stream object around it (CPU-only builds of
+# torch do not have it; no tensor is on a device there).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if torch.cuda.is_initialized() and _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -162,7 +169,7 @@ def _check(t, name, dtype, shape=None, optional=False):
         raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -171,21 +178,22 @@ def _check(t, name, dtype, shape=None, optional=False):
 def _on_device(**tensors):
     """Every given tensor lives on the current CUDA device (checked after the
     dtypes and shapes of all of them)."""
+    current = None
     for name, t in tensors.items():
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, but the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+        if current is None:
+            current = torch.cuda.current_device()
+        if t.get_device() != current:
+            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{current}")
 
 
 def _check_workspace(ws, need: int):
     _check(ws, "workspace", None)
-    if ws.numel() * ws.element_size() < need:
-        raise ValueError(f"workspace holds {ws.numel() * ws.element_size()} bytes, "
-                         f"{need} needed")
+    if ws.nbytes < need:
+        raise ValueError(f"workspace holds {ws.nbytes} bytes, {need} needed")
 
 
 def _dims2(t, name):
@@ -387,14 +395,16 @@ def _check_rows(t, name, heads=None, D=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
     _bf16(t, name)
-    if t.dim() != 3 or (heads is not None and tuple(t.shape[1:]) != (heads, D)):
+    if t.dim() != 3 or (heads is not None and t.shape[1:] != (heads, D)):
         raise ValueError(f"{name} must have shape [tokens, {heads or 'heads'}, {D or 'D'}], got {tuple(t.shape)}")
     T, h, d = t.shape
     if T == 0:
         return h * d
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+    stride, head, one = t.stride()
+    if one != 1 or (h > 1 and head != d):
         raise ValueError(f"the heads of a token must be contiguous in {name}")
-    stride = t.stride(0) if T > 1 else h * d
+    if T == 1:
+        return h * d
     if stride < h * d:
         raise ValueError(f"tokens overlap in {name}")
     return stride
@@ -441,10 +451,10 @@ def fmlp_rope_append(q, k, v, cu_seqlens, kv_len, rope, q_out, k_cache, v_cache,
                                                        workspace, q_gamma, k_gamma, torch.bfloat16)
     _on_device(q=q, k=k, v=v, cu_seqlens=cu_seqlens, kv_len=kv_len, q_gamma=q_gamma, k_gamma=k_gamma, q_out=q_out,
                k_cache=k_cache, v_cache=v_cache, workspace=workspace)
-    _check_status(lib.fmlp_rope_append(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, _ptr(cu_seqlens),
-                                       _ptr(kv_len), B, H, H_kv, D, ctypes.byref(rope._c), _ptr(q_gamma),
-                                       _ptr(k_gamma), eps, _ptr(q_out), _ptr(k_cache), _ptr(v_cache), n_max,
-                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
+    _check_status(lib.fmlp_rope_append(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, cu_seqlens.data_ptr(),
+                                       kv_len.data_ptr(), B, H, H_kv, D, ctypes.byref(rope._c), _ptr(q_gamma),
+                                       _ptr(k_gamma), eps, q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), n_max,
+                                       workspace.data_ptr(), workspace.nbytes,
                                        _stream(stream)),
                   "fmlp_rope_append")
 
@@ -459,11 +469,11 @@ def fmlp_rope_append_q8(q, k, v, cu_seqlens, kv_len, rope, q_out, k_q, k_s, v_q,
     _check(v_s, "v_s", torch.float32, (B, H_kv, n_max))
     _on_device(q=q, k=k, v=v, cu_seqlens=cu_seqlens, kv_len=kv_len, q_gamma=q_gamma, k_gamma=k_gamma, q_out=q_out,
                k_q=k_q, k_s=k_s, v_q=v_q, v_s=v_s, workspace=workspace)
-    _check_status(lib.fmlp_rope_append_q8(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, _ptr(cu_seqlens),
-                                          _ptr(kv_len), B, H, H_kv, D, ctypes.byref(rope._c), _ptr(q_gamma),
-                                          _ptr(k_gamma), eps, _ptr(q_out), _ptr(k_q), _ptr(k_s), _ptr(v_q),
-                                          _ptr(v_s), n_max, _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), _stream(stream)),
+    _check_status(lib.fmlp_rope_append_q8(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, cu_seqlens.data_ptr(),
+                                          kv_len.data_ptr(), B, H, H_kv, D, ctypes.byref(rope._c), _ptr(q_gamma),
+                                          _ptr(k_gamma), eps, q_out.data_ptr(), k_q.data_ptr(), k_s.data_ptr(), v_q.data_ptr(),
+                                          v_s.data_ptr(), n_max, workspace.data_ptr(),
+                                          workspace.nbytes, _stream(stream)),
                   "fmlp_rope_append_q8")
 
 
@@ -487,9 +497,9 @@ def fmlp_kv_read_q8(k_q, k_s, v_q, v_s, kv_len, k_cache, v_cache, workspace, str
     _check_workspace(workspace, CONTROL_BYTES)
     _on_device(k_q=k_q, k_s=k_s, v_q=v_q, v_s=v_s, kv_len=kv_len, k_cache=k_cache, v_cache=v_cache,
                workspace=workspace)
-    _check_status(lib.fmlp_kv_read_q8(_ptr(k_q), _ptr(k_s), _ptr(v_q), _ptr(v_s), _ptr(kv_len), B, H_kv, D, n_max,
-                                      _ptr(k_cache), _ptr(v_cache), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream(stream)),
+    _check_status(lib.fmlp_kv_read_q8(k_q.data_ptr(), k_s.data_ptr(), v_q.data_ptr(), v_s.data_ptr(), kv_len.data_ptr(), B, H_kv, D, n_max,
+                                      k_cache.data_ptr(), v_cache.data_ptr(), workspace.data_ptr(),
+                                      workspace.nbytes, _stream(stream)),
                   "fmlp_kv_read_q8")
 
 
@@ -515,9 +525,9 @@ def fmlp_attn_prefill(q, k_cache, v_cache, cu_seqlens, kv_len, scale: float, out
     _check_workspace(workspace, fmlp_prefill_workspace_bytes(T, B, H, H_kv, D))
     _on_device(q=q, k_cache=k_cache, v_cache=v_cache, cu_seqlens=cu_seqlens, kv_len=kv_len, out=out,
                workspace=workspace)
-    _check_status(lib.fmlp_attn_prefill(q.data_ptr(), q_stride, _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens),
-                                        _ptr(kv_len), T, B, H, H_kv, D, n_max, scale, _ptr(out), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(), _stream(stream)),
+    _check_status(lib.fmlp_attn_prefill(q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), cu_seqlens.data_ptr(),
+                                        kv_len.data_ptr(), T, B, H, H_kv, D, n_max, scale, out.data_ptr(), workspace.data_ptr(),
+                                        workspace.nbytes, _stream(stream)),
                   "fmlp_attn_prefill")
 
 
@@ -541,9 +551,9 @@ def fmlp_attn_decode_q8(q, k_q, k_s, v_q, v_s, kv_len, scale: float, out, worksp
     _check(out, "out", torch.float32, (B, H, D))
     _check_workspace(workspace, fmlp_attn_q8_workspace_bytes(B, H, H_kv, D))
     _on_device(q=q, k_q=k_q, k_s=k_s, v_q=v_q, v_s=v_s, kv_len=kv_len, out=out, workspace=workspace)
-    _check_status(lib.fmlp_attn_decode_q8(_ptr(q), _ptr(k_q), _ptr(k_s), _ptr(v_q), _ptr(v_s), _ptr(kv_len), B, H,
-                                          H_kv, D, n_max, scale, _ptr(out), _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), _stream(stream)),
+    _check_status(lib.fmlp_attn_decode_q8(q.data_ptr(), k_q.data_ptr(), k_s.data_ptr(), v_q.data_ptr(), v_s.data_ptr(), kv_len.data_ptr(), B, H,
+                                          H_kv, D, n_max, scale, out.data_ptr(), workspace.data_ptr(),
+                                          workspace.nbytes, _stream(stream)),
                   "fmlp_attn_decode_q8")
 
 
