@@ -34,7 +34,8 @@
 namespace fmlp {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendBatch = 3;  // rows of a lane group on their way at once
 constexpr int kReadThreads = 256;
 constexpr int kReadRows = 64;  // rows of a tile of kv_read_q8
 
@@ -111,8 +112,35 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
+// Sequence and position of token t, by one warp: position -1 for a token that is passed
+// over (in no sequence, padding, or of a refused sequence).
+__device__ __forceinline__ int place(const AppendParams& p, int64_t t, int lane, int64_t& b) {
+  int64_t c0, c1, len;
+  if (p.B < 32) {  // every length in one round trip
+    const int64_t c = __ldg(p.cu + min((int64_t)lane, p.B));
+    const int64_t n = __ldg(p.kv_len + min((int64_t)lane, p.B - 1));
+    const int64_t first = __shfl_sync(0xffffffffu, c, 0), end = __shfl_sync(0xffffffffu, c, (int)p.B);
+    if (t < first || t >= end) return -1;
+    b = max(__popc(__ballot_sync(0xffffffffu, lane < p.B && c <= t)), 1) - 1;
+    c0 = __shfl_sync(0xffffffffu, c, (int)b);
+    c1 = __shfl_sync(0xffffffffu, c, (int)b + 1);
+    len = __shfl_sync(0xffffffffu, n, (int)b);
+  } else {
+    if (t < __ldg(p.cu) || t >= __ldg(p.cu + p.B)) return -1;
+    b = sequence_of(p.cu, p.B, t, lane);
+    c0 = __ldg(p.cu + b);
+    c1 = __ldg(p.cu + b + 1);
+    len = __ldg(p.kv_len + b);
+  }
+  if (t < c0 || t >= c1 || len < 0 || len > p.n_max) {
+    if (lane == 0) atomicOr(p.status, kStatusBadInput);
+    return -1;
+  }
+  return (int)max(len - (c1 - t), (int64_t)-1);
+}
+
 template <int D, bool kQ8>
-__global__ void __launch_bounds__(kAppendThreads) rope_append(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 8) rope_append(const __grid_constant__ AppendParams p) {
   constexpr int L = D == 64 ? 4 : 8;   // lanes per row
   constexpr int kUnits = D / 16;       // of them at work (6 of 8 for D = 96)
   constexpr int kGroups = kAppendThreads / L;
@@ -125,29 +153,6 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append(const __grid_const
 
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x;
-  if (tid < 32) {
-    const int64_t first = __ldg(p.cu), end = __ldg(p.cu + p.B);
-    int pos = -1;
-    int64_t b = 0;
-    if (t >= first && t < end) {
-      b = sequence_of(p.cu, p.B, t, tid);
-      const int64_t c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), len = __ldg(p.kv_len + b);
-      if (t < c0 || t >= c1 || len < 0 || len > p.n_max) {
-        if (tid == 0) atomicOr(p.status, kStatusBadInput);
-      } else {
-        pos = (int)max(len - (c1 - t), (int64_t)-1);  // negative: padding, passed over
-      }
-    }
-    if (tid == 0) {
-      s_seq = b;
-      s_pos = pos;
-    }
-  }
-  __syncthreads();
-  const int pos = s_pos;
-  if (pos < 0) return;
-  const int64_t b = s_seq;
-
   // this lane's two 8-value pieces of a row
   const int u = tid % L, ru = p.R / 16;
   const bool works = u < kUnits, rotates = u < ru;
@@ -157,22 +162,36 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append(const __grid_const
   const int rows = p.H + 2 * p.H_kv;
   const int per = (rows + gridDim.y - 1) / gridDim.y;
   const int r0 = blockIdx.y * per, r1 = min(rows, r0 + per);
-  bool table = false;
-  for (int base = r0; base < r1; base += kGroups) {
-    const int r = base + tid / L;
-    const bool live = works && r < r1;
-    const bool is_q = r < p.H, is_v = r >= p.H + p.H_kv;
-    const int g = is_q ? r : is_v ? r - p.H - p.H_kv : r - p.H;
-    const __nv_bfloat16* src = is_q   ? p.q + t * p.q_stride + (int64_t)g * D
-                               : is_v ? p.v + t * p.v_stride + (int64_t)g * D
-                                      : p.k + t * p.k_stride + (int64_t)g * D;
-    uint4 w0 = {}, w1 = {};
-    if (live) {
-      w0 = *reinterpret_cast<const uint4*>(src + 8 * c0);
-      w1 = *reinterpret_cast<const uint4*>(src + 8 * c1);
+  int64_t b = 0;
+  int pos = -1;
+  for (int base = r0; base < r1; base += kAppendBatch * kGroups) {
+    // the rows of a batch, asked for before anything else
+    uint4 w0[kAppendBatch], w1[kAppendBatch];
+#pragma unroll
+    for (int i = 0; i < kAppendBatch; ++i) {
+      const int r = base + i * kGroups + tid / L;
+      const __nv_bfloat16* src =
+          r < p.H ? p.q + t * p.q_stride + (int64_t)r * D
+                  : r < p.H + p.H_kv ? p.k + t * p.k_stride + (int64_t)(r - p.H) * D
+                                     : p.v + t * p.v_stride + (int64_t)(r - p.H - p.H_kv) * D;
+      w0[i] = w1[i] = make_uint4(0, 0, 0, 0);
+      if (works && r < r1) {
+        w0[i] = *reinterpret_cast<const uint4*>(src + 8 * c0);
+        w1[i] = *reinterpret_cast<const uint4*>(src + 8 * c1);
+      }
     }
-    if (!table) {  // while the first rows are on their way
-      table = true;
+    if (base == r0) {  // meanwhile: the token's place, then its cosines and sines
+      if (tid < 32) {
+        const int at = place(p, t, tid, b);
+        if (tid == 0) {
+          s_seq = b;
+          s_pos = at;
+        }
+      }
+      __syncthreads();
+      pos = s_pos;
+      if (pos < 0) return;
+      b = s_seq;
       for (int i = tid; i < p.R / 2; i += kAppendThreads) {
         double s, c;
         sincos((double)pos * p.freq[i], &s, &c);
@@ -181,66 +200,74 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append(const __grid_const
       }
       __syncthreads();
     }
-    Chunk x0 = unpack(w0), x1 = unpack(w1);
-    const __nv_bfloat16* gamma = is_q ? p.q_gamma : p.k_gamma;
-    if (p.q_gamma || p.k_gamma) {  // uniform over the CTA: the shuffles need every lane
-      float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x0.x[j], x0.x[j], fmaf(x1.x[j], x1.x[j], ss));
-      ss = group_sum<L>(ss);
-      if (live && !is_v && gamma) {
-        const float rinv = 1.0f / sqrtf(ss / (float)D + p.eps);
-        const Chunk g0 = unpack(ld_keep(gamma + 8 * c0)), g1 = unpack(ld_keep(gamma + 8 * c1));
+    for (int i = 0; i < kAppendBatch; ++i) {
+      if (base + i * kGroups >= r1) break;  // uniform: the shuffles below need every lane
+      const int r = base + i * kGroups + tid / L;
+      const bool live = works && r < r1;
+      const bool is_q = r < p.H, is_v = r >= p.H + p.H_kv;
+      const int g = is_q ? r : is_v ? r - p.H - p.H_kv : r - p.H;
+      Chunk x0 = unpack(w0[i]), x1 = unpack(w1[i]);
+      const __nv_bfloat16* gamma = is_q ? p.q_gamma : p.k_gamma;
+      if (p.q_gamma || p.k_gamma) {
+        float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x0.x[j] *= rinv * g0.x[j];
-          x1.x[j] *= rinv * g1.x[j];
+        for (int j = 0; j < 8; ++j) ss = fmaf(x0.x[j], x0.x[j], fmaf(x1.x[j], x1.x[j], ss));
+        ss = group_sum<L>(ss);
+        if (live && !is_v && gamma) {
+          const float rinv = 1.0f / sqrtf(ss / (float)D + p.eps);
+          const Chunk g0 = unpack(ld_keep(gamma + 8 * c0)), g1 = unpack(ld_keep(gamma + 8 * c1));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x0.x[j] *= rinv * g0.x[j];
+            x1.x[j] *= rinv * g1.x[j];
+          }
         }
       }
-    }
-    if (rotates && !is_v) {
-      if (p.interleaved) {
+      if (rotates && !is_v) {
+        if (p.interleaved) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float ca = cs[8 * u + j], sa = sn[8 * u + j];
-          const float cb = cs[8 * u + 4 + j], sb = sn[8 * u + 4 + j];
-          const float a = x0.x[2 * j], b2 = x0.x[2 * j + 1], c = x1.x[2 * j], d = x1.x[2 * j + 1];
-          x0.x[2 * j] = a * ca - b2 * sa;
-          x0.x[2 * j + 1] = a * sa + b2 * ca;
-          x1.x[2 * j] = c * cb - d * sb;
-          x1.x[2 * j + 1] = c * sb + d * cb;
+          for (int j = 0; j < 4; ++j) {
+            const float ca = cs[8 * u + j], sa = sn[8 * u + j];
+            const float cb = cs[8 * u + 4 + j], sb = sn[8 * u + 4 + j];
+            const float a0 = x0.x[2 * j], a1 = x0.x[2 * j + 1], b0 = x1.x[2 * j], b1 = x1.x[2 * j + 1];
+            x0.x[2 * j] = a0 * ca - a1 * sa;
+            x0.x[2 * j + 1] = a0 * sa + a1 * ca;
+            x1.x[2 * j] = b0 * cb - b1 * sb;
+            x1.x[2 * j + 1] = b0 * sb + b1 * cb;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float c = cs[8 * u + j], s = sn[8 * u + j], a0 = x0.x[j], a1 = x1.x[j];
+            x0.x[j] = a0 * c - a1 * s;
+            x1.x[j] = a0 * s + a1 * c;
+          }
         }
+      }
+      float s = 0.f;
+      if (kQ8) {
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(x0.x[j]), fabsf(x1.x[j])));
+        s = __fdiv_rn(group_max<L>(m), 127.f);
+      }
+      if (!live) continue;
+      const int64_t row = (b * p.H_kv + g) * p.n_max + pos;  // of the cache, for k and v
+      if (is_q) {
+        __nv_bfloat16* dst = p.q_out + (t * p.H + g) * D;
+        *reinterpret_cast<uint4*>(dst + 8 * c0) = pack(x0);
+        *reinterpret_cast<uint4*>(dst + 8 * c1) = pack(x1);
+      } else if (kQ8) {
+        int8_t* dst = (is_v ? p.v_q : p.k_q) + row * D;
+        *reinterpret_cast<uint2*>(dst + 8 * c0) = codes(x0, s);
+        *reinterpret_cast<uint2*>(dst + 8 * c1) = codes(x1, s);
+        if (u == 0) (is_v ? p.v_s : p.k_s)[row] = s;
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float c = cs[8 * u + j], s = sn[8 * u + j], a = x0.x[j], d = x1.x[j];
-          x0.x[j] = a * c - d * s;
-          x1.x[j] = a * s + d * c;
-        }
+        __nv_bfloat16* dst = (is_v ? p.v_cache : p.k_cache) + row * D;
+        *reinterpret_cast<uint4*>(dst + 8 * c0) = is_v ? w0[i] : pack(x0);
+        *reinterpret_cast<uint4*>(dst + 8 * c1) = is_v ? w1[i] : pack(x1);
       }
-    }
-    const int64_t row = (b * p.H_kv + g) * p.n_max + pos;  // of the cache, for k and v
-    float s = 0.f;
-    if (kQ8) {
-      float m = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(x0.x[j]), fabsf(x1.x[j])));
-      s = __fdiv_rn(group_max<L>(m), 127.f);
-    }
-    if (!live) continue;
-    if (is_q) {
-      __nv_bfloat16* dst = p.q_out + (t * p.H + g) * D;
-      *reinterpret_cast<uint4*>(dst + 8 * c0) = pack(x0);
-      *reinterpret_cast<uint4*>(dst + 8 * c1) = pack(x1);
-    } else if (kQ8) {
-      int8_t* dst = (is_v ? p.v_q : p.k_q) + row * D;
-      *reinterpret_cast<uint2*>(dst + 8 * c0) = codes(x0, s);
-      *reinterpret_cast<uint2*>(dst + 8 * c1) = codes(x1, s);
-      if (u == 0) (is_v ? p.v_s : p.k_s)[row] = s;
-    } else {
-      __nv_bfloat16* dst = (is_v ? p.v_cache : p.k_cache) + row * D;
-      *reinterpret_cast<uint4*>(dst + 8 * c0) = is_v ? w0 : pack(x0);
-      *reinterpret_cast<uint4*>(dst + 8 * c1) = is_v ? w1 : pack(x1);
     }
   }
 }
