@@ -412,9 +412,9 @@ FMLP_API fmlp_status fmlp_rope_append(const void* q, int64_t q_stride, const voi
  * fmlp_rope_append_q8 -- the same into an int8 cache, this library's own
  * format: each row x (D values of one head) is held as one binary32 scale
  *     s = fl32(max |x| / 127)
- * and D int8 codes clamp(rint(fl32(x / s)), -127, 127) (0 in a row of zeros),
- * taken from the f32 values after norm and rotation.  A row stands for
- * codes * s.
+ * and D int8 codes rint(x * fl32(1 / s)), within +-127, taken from the f32
+ * values after norm and rotation.  A row stands for codes * s, which is within
+ * (0.5 + 2^-15) s of x.  A row whose s would be under 2^-125 is held as zeros.
  *
  *   k_q, v_q : int8 [B x H_kv x n_max x D]
  *   k_s, v_s : f32 [B x H_kv x n_max]

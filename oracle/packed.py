@@ -62,6 +62,7 @@ def quantize_kv(x):
     """int8 codes and binary32 scales of rows x [..., D]."""
     x = np.asarray(x, dtype=np.float64)
     s = (np.max(np.abs(x), axis=-1) / 127).astype(np.float32)
+    s = np.where(s < 2.0 ** -125, np.float32(0), s)
     safe = np.where(s > 0, s, 1).astype(np.float64)
     q = np.where(s[..., None] > 0, np.clip(np.rint(x / safe[..., None]), -127, 127), 0)
     return q.astype(np.int8), s

@@ -257,3 +257,24 @@ def test_captured_and_replayed_with_other_lengths(fm, cuda_device):
     got = dec(s["q_out"])
     for t, r in enumerate(reference(s, rot, False, "q")):
         assert np.all(np.abs(got[t] - r[0]) <= 2.0 ** -8 * np.abs(r[0]) + r[1])
+
+
+def test_q8_rows_of_any_size(fm, cuda_device):
+    """Rows from the smallest numbers to the largest: each within half a step (and 2^-15 of it) of its
+    scale, rows under the smallest scale held as zeros, none NaN."""
+    D, sizes = 64, [0.0, 1e-40, 1e-37, 2e-36, 1e-30, 1.0, 1e30, 3e38]
+    s = batch(cuda_device, [(len(sizes), len(sizes))], 1, 1, D, len(sizes), seed=9)
+    v = torch.linspace(-1, 1, D, dtype=torch.float64)[None] * torch.tensor(sizes, dtype=torch.float64)[:, None]
+    s["v"] = v.to(torch.bfloat16)[:, None].to(cuda_device)
+    codes = {c: torch.ones(1, 1, len(sizes), D, dtype=torch.int8, device=cuda_device) for c in "kv"}
+    scales = {c: torch.ones(1, 1, len(sizes), device=cuda_device) for c in "kv"}
+    fm.fmlp_rope_append_q8(s["q"].contiguous(), s["k"].contiguous(), s["v"], s["cu"], s["kv_len"], fm.FmlpRope(1e4, D),
+                           s["q_out"], codes["k"], scales["k"], codes["v"], scales["v"], s["ws"])
+    x, q, sc = dec(s["v"])[:, 0], codes["v"][0, 0].cpu().double().numpy(), scales["v"][0, 0].cpu().double().numpy()
+    top = np.max(np.abs(x), axis=1)
+    small = (top / 127).astype(np.float32) < 2.0 ** -125
+    assert np.all(sc[small] == 0) and np.all(q[small] == 0)
+    assert small.sum() == 4                      # 0, 1e-40, 1e-37, 2e-36: under 127 * 2^-125 = 2.98e-36
+    err = np.abs(q * sc[:, None] - x)[~small]
+    assert np.all(err <= (0.5 + 2.0 ** -15) * sc[~small][:, None]) and np.all(np.isfinite(sc))
+    assert np.all(np.max(np.abs(q[~small]), axis=1) == 127)

@@ -10,7 +10,7 @@
 //     once; the rotation itself is f32;
 //   * q is rounded to bf16 into q_out; k and v go to row p of their head's
 //     cache region, as bf16 (v a bit copy), or as int8 codes with one f32
-//     scale a row: s = fl32(max |x| / 127), code = rint(fl32(x / s)), taken
+//     scale a row: s = fl32(max |x| / 127), code = rint(x fl32(1 / s)), taken
 //     from the f32 values, so a key is rounded once.
 // Bound by HBM for prompts (each row read once and written once) and by the
 // latency of one launch for decode steps.
@@ -23,7 +23,7 @@
 // and the norm and the row maximum take two or three shuffles.
 //
 // kv_read_q8: rows [0, kv_len) of an int8 cache as bf16 (code times scale, in
-// f32, rounded once).  HBM-bound; every CTA walks 64-row tiles of all
+// f32, rounded once).  HBM-bound; every CTA walks 128-row tiles of all
 // (sequence, head) regions, lengths taken from the device.
 #include "common.cuh"
 #include "internal.h"
@@ -37,7 +37,7 @@ namespace {
 constexpr int kAppendThreads = 128;
 constexpr int kAppendBatch = 3;  // rows of a lane group on their way at once
 constexpr int kReadThreads = 256;
-constexpr int kReadRows = 64;  // rows of a tile of kv_read_q8
+constexpr int kReadRows = 128;  // rows of a tile of kv_read_q8
 
 struct AppendParams {
   const __nv_bfloat16 *q, *k, *v;  // rows of a token start at multiples of the strides
@@ -91,13 +91,18 @@ __device__ __forceinline__ uint4 pack(const Chunk& c) {
   return make_uint4(pack2(c.x[0], c.x[1]), pack2(c.x[2], c.x[3]), pack2(c.x[4], c.x[5]),
                     pack2(c.x[6], c.x[7]));
 }
-__device__ __forceinline__ uint32_t code(float x, float s) {
-  const float q = s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
-  return (uint32_t)(int)fminf(fmaxf(q, -127.f), 127.f) & 0xffu;
-}
-__device__ __forceinline__ uint2 codes(const Chunk& c, float s) {
-  return make_uint2(code(c.x[0], s) | code(c.x[1], s) << 8 | code(c.x[2], s) << 16 | code(c.x[3], s) << 24,
-                    code(c.x[4], s) | code(c.x[5], s) << 8 | code(c.x[6], s) << 16 | code(c.x[7], s) << 24);
+// rint(x * inv) of 8 values as bytes (|x * inv| < 127.5): adding 1.5 * 2^23 to the exact
+// product rounds it to an integer whose two's complement is in the low bits.  (Dividing
+// each value by the scale instead made the kernel bound by its instructions.)
+__device__ __forceinline__ uint2 codes(const Chunk& c, float inv) {
+  constexpr float kMagic = 12582912.f;
+  uint32_t t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t[j] = __float_as_uint(fmaf(c.x[j], inv, kMagic));
+  const auto join = [&](int i) {
+    return __byte_perm(__byte_perm(t[i], t[i + 1], 0x0040), __byte_perm(t[i + 2], t[i + 3], 0x0040), 0x5410);
+  };
+  return make_uint2(join(0), join(4));
 }
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
@@ -245,12 +250,16 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append(const __grid_co
           }
         }
       }
-      float s = 0.f;
+      float s = 0.f, inv = 0.f;
       if (kQ8) {
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(x0.x[j]), fabsf(x1.x[j])));
         s = __fdiv_rn(group_max<L>(m), 127.f);
+        if (s < 0x1p-125f)
+          s = 0.f;  // its reciprocal may overflow
+        else
+          inv = __frcp_rn(s);
       }
       if (!live) continue;
       const int64_t row = (b * p.H_kv + g) * p.n_max + pos;  // of the cache, for k and v
@@ -260,8 +269,8 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append(const __grid_co
         *reinterpret_cast<uint4*>(dst + 8 * c1) = pack(x1);
       } else if (kQ8) {
         int8_t* dst = (is_v ? p.v_q : p.k_q) + row * D;
-        *reinterpret_cast<uint2*>(dst + 8 * c0) = codes(x0, s);
-        *reinterpret_cast<uint2*>(dst + 8 * c1) = codes(x1, s);
+        *reinterpret_cast<uint2*>(dst + 8 * c0) = codes(x0, inv);
+        *reinterpret_cast<uint2*>(dst + 8 * c1) = codes(x1, inv);
         if (u == 0) (is_v ? p.v_s : p.k_s)[row] = s;
       } else {
         __nv_bfloat16* dst = (is_v ? p.v_cache : p.k_cache) + row * D;
@@ -307,8 +316,9 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_q8(const __grid_constant
       const int n = len[i], per_head = (n + kReadRows - 1) / kReadRows;
       const int64_t tiles = (int64_t)per_head * p.H_kv;
       for (; w < base + tiles; w += gridDim.x) {
-        const int64_t seg = (b0 + i) * p.H_kv + (w - base) / per_head;
-        const int row0 = (int)((w - base) % per_head) * kReadRows;
+        const uint32_t at = (uint32_t)(w - base);  // a cache of 2^32 tiles is past any memory
+        const int64_t seg = (b0 + i) * p.H_kv + at / (uint32_t)per_head;
+        const int row0 = (int)(at % (uint32_t)per_head) * kReadRows;
         const int64_t r0 = seg * p.n_max + row0;
         const int pieces = min(kReadRows, n - row0) * (D / 16);
         uint4 kw[kPer], vw[kPer];
@@ -334,9 +344,14 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_q8(const __grid_constant
             uint32_t o[8];
 #pragma unroll
             for (int i4 = 0; i4 < 4; ++i4) {
-              const char4 c = *reinterpret_cast<const char4*>(&in[i4]);
-              o[2 * i4] = pack2((float)c.x * s, (float)c.y * s);
-              o[2 * i4 + 1] = pack2((float)c.z * s, (float)c.w * s);
+              // byte b + 128 as the low byte of 2^23, less 2^23 + 128: exact
+              const uint32_t c = in[i4] ^ 0x80808080u;
+              const float f0 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7440)) - 8388736.f;
+              const float f1 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7441)) - 8388736.f;
+              const float f2 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7442)) - 8388736.f;
+              const float f3 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7443)) - 8388736.f;
+              o[2 * i4] = pack2(f0 * s, f1 * s);
+              o[2 * i4 + 1] = pack2(f2 * s, f3 * s);
             }
             uint4* dst = reinterpret_cast<uint4*>((kv ? p.v_out : p.k_out) + r0 * D) + 2 * e;
             dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
