@@ -52,10 +52,7 @@ constexpr int kQ8Header = 1024;
 constexpr int kQ8MaxCtas = 256;
 // A region costs its units and, to start and to finish, about as much as this many
 // more; the shares of the CTAs are counted in both.
-#ifndef Q8_REGION
-#define Q8_REGION 4
-#endif
-constexpr int kRegionCost = Q8_REGION;
+constexpr int kRegionCost = 4;
 
 struct Q8Params {
   CUtensorMap k_map, v_map;  // int8 [B H_kv][n_max][D], box 1 x 128 x 128

@@ -62,14 +62,7 @@ constexpr int kPfHeader = 1024;
 constexpr float kRescaleAbove = 8.f;
 // An item costs its units and, to start (Q, the first K) and to finish (O), about as
 // much as this many more; the shares of the CTAs are counted in both.
-#ifndef PF_ITEM
-#define PF_ITEM 2
-#endif
-constexpr int kPfItemCost = PF_ITEM;
-#ifndef PF_FMA
-#define PF_FMA 0
-#endif
-constexpr int kPfFma = PF_FMA;
+constexpr int kPfItemCost = 2;
 // TMEM columns: S of the two tiles in halves of 64 (W over the first 32 of each), O of them
 constexpr uint32_t kColS = 0, kColO = 256, kPfTmemCols = 512;
 
@@ -307,39 +300,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// 2^x of a pair on the FMA pipes, for -120 <= x (smaller ones give 2^-120): adding
-// 1.5 * 2^23 rounds x to an integer n, a cubic (fitted for the least largest relative
-// error over [-1/2, 1/2], 7.5e-5, against the 2^-9 of the rounding to bf16 that follows)
-// gives 2^(x - n), and n goes into the exponent bits.
-__device__ __forceinline__ void ex2_fma(float& x, float& y) {
-  constexpr float kMagic = 12582912.f;
-  const uint64_t v = pk2(fmaxf(x, -120.f), fmaxf(y, -120.f));
-  const uint64_t t = fadd2(v, pk2(kMagic, kMagic));
-  const uint64_t f = ffma2(fadd2(t, pk2(-kMagic, -kMagic)), pk2(-1.f, -1.f), v);
-  uint64_t q = ffma2(pk2(0.05517167f, 0.05517167f), f, pk2(0.24261113f, 0.24261113f));
-  q = ffma2(q, f, pk2(0.69326099f, 0.69326099f));
-  q = ffma2(q, f, pk2(0.99992807f, 0.99992807f));
-  float n0, n1, q0, q1;
-  unpk2(t, n0, n1);
-  unpk2(q, q0, q1);
-  x = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(n0) << 23));
-  y = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(n1) << 23));
-}
-// s[0..63] <- w = 2^(s sc + nref) as 32 bf16 pairs in s[0..31]; sum += w.  kFma of every
-// eight pairs take the FMA pipes, the others the exp2 unit.
-template <int kFma>
+// s[0..63] <- w = 2^(s sc + nref) as 32 bf16 pairs in s[0..31]; sum += w.  (A quarter of
+// the exponentials as polynomials on the FMA pipes made an 8192-token prompt 4% slower:
+// the exp2 unit is not what the kernel waits for.)
 __device__ __forceinline__ void weights(uint32_t (&s)[64], uint64_t sc2, uint64_t nref2,
                                         uint64_t (&sum)[2]) {
 #pragma unroll
   for (int i = 0; i < 64; i += 2) {
     float x, y;
     unpk2(ffma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, nref2), x, y);
-    if ((i >> 1) % 8 < kFma) {
-      ex2_fma(x, y);
-    } else {
-      x = ex2(x);
-      y = ex2(y);
-    }
+    x = ex2(x);
+    y = ex2(y);
     sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], pk2(x, y));
     s[i >> 1] = bf16x2(x, y);
   }
@@ -624,8 +595,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
             tmem_ld<32>(s_addr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
             tmem_wait();
             const int cols = rows - j * kTile - h * 64;
-            const bool cut = __any_sync(0xffffffffu, cols < 64);
-            if (cut) {
+            if (__any_sync(0xffffffffu, cols < 64)) {
 #pragma unroll
               for (int i = 0; i < 64; ++i)
                 if (i >= cols) s[i] = 0xff800000u;  // -inf
@@ -661,10 +631,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
             const float ref = m == -CUDART_INF_F ? 0.f : m;
             const uint64_t sc2 = pk2(p.scale_log2, p.scale_log2), ref2 = pk2(-ref, -ref);
             uint64_t sum[2] = {0ull, 0ull};
-            if (cut)
-              weights<0>(s, sc2, ref2, sum);  // masked scores give exact zeros
-            else
-              weights<kPfFma>(s, sc2, ref2, sum);
+            weights(s, sc2, ref2, sum);
             tmem_st32(s_addr + h * 64, s);
             l += hsum2(fadd2(sum[0], sum[1]));
             tmem_st_wait();
@@ -768,10 +735,11 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
               L = fmaf(exp2f(__ldcg(piece(c) + r) - M), __ldcg(piece(c) + p.piece_rows + r), L);
             const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
 #pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += 32) {  // 8 loads of a piece in flight
+            for (int d0 = 0; d0 < D; d0 += 32) {  // 8 loads of each of two pieces in flight
               float acc[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+#pragma unroll 2
               for (int c = cf; c <= cl; ++c) {
                 const float* pc = piece(c);
                 const float4* src = reinterpret_cast<const float4*>(pc + 2 * p.piece_rows) + (size_t)(d0 / 4) * p.piece_rows + r;
