@@ -333,7 +333,10 @@ FMLP_API fmlp_status fmlp_attn_decode(const void* q, const void* k_new, const vo
  *                its i-th one stands at position p = kv_len[b] - n_b + i, which
  *                is also its row of the cache.  A token with p < 0 is padding.
  *   workspace  : its first 256 bytes (FMLP_CONTROL_BYTES) are control words;
- *                zero-fill it once.  Read fmlp_device_status as for the other
+ *                zero-fill it once.  One workspace, of the largest size that any
+ *                of them needs, serves all the packed-batch calls in any order;
+ *                zero-fill it again after a call of another kind used it
+ *                (fmlp_forward, fmlp_attn_decode, ...).  Read fmlp_device_status as for the other
  *                calls: a sequence whose kv_len is outside [0, n_max], or whose
  *                cu_seqlens decrease or leave [0, T], is not processed (its
  *                outputs and cache stay as they were) and is reported as

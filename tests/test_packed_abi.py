@@ -150,5 +150,5 @@ def test_attn_q8_workspace_and_refusals():
     for bad in (dict(q=None), dict(q=MIS), dict(kq=None), dict(kq=MIS), dict(ks=None), dict(vs=MIS4), dict(vq=MIS),
                 dict(kv=None), dict(kv=MIS4), dict(B=0), dict(H=3), dict(H=34), dict(D=32), dict(n_max=0),
                 dict(scale=-1.0), dict(scale=float("nan")), dict(out=None), dict(out=MIS), dict(out=A + 32),
-                dict(ws=None), dict(wsb=300)):
+                dict(kq=0x900000), dict(vs=0x900100), dict(ws=None), dict(wsb=300)):
         assert attend(**bad) == fm.FMLP_ERR_INVALID_ARG, bad

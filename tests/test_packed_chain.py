@@ -170,3 +170,32 @@ def test_two_streams_with_their_own_workspaces(fm, cuda_device):
     for s in work:
         assert fm.fmlp_device_status(s["ws"]) == fm.FMLP_OK
         check_prefill(s["out"], s["q"], s["k"], s["v"], [0, 20, 21, 60], [300, 77, 200], scale)
+
+
+def test_one_workspace_for_all_calls_in_any_order(fm, cuda_device):
+    """Prompt attention and int8 decode attention, both split over many CTAs, take turns on one
+    workspace: each finds its counters as it needs them."""
+    dev, scale, n = cuda_device, 1 / math.sqrt(D), 6000
+    ws = torch.zeros(max(fm.fmlp_prefill_workspace_bytes(150, 1, H, H_KV, D),
+                         fm.fmlp_attn_q8_workspace_bytes(1, H, H_KV, D)), dtype=torch.uint8, device=dev)
+    kc, vc = (wl.normal_bf16(9, i, (1, H_KV, n, D)).to(dev) for i in (72, 73))
+    kq, vq = (torch.randint(-127, 128, (1, H_KV, n, D), dtype=torch.int8, device=dev) for _ in range(2))
+    ks, vs = (torch.rand(1, H_KV, n, device=dev) / 64 for _ in range(2))
+    q = wl.normal_bf16(9, 74, (150, H, D)).to(dev)
+    cu, lens = i32(dev, [0, 150]), i32(dev, [n])
+    out, one = torch.empty(150, H, D, dtype=torch.bfloat16, device=dev), torch.empty(1, H, D, device=dev)
+    seen = []
+    for _ in range(4):
+        fm.fmlp_attn_prefill(q, kc, vc, cu, lens, scale, out, ws)
+        fm.fmlp_attn_decode_q8(q[:1], kq, ks, vq, vs, lens, scale, one, ws)
+        assert fm.fmlp_device_status(ws) == fm.FMLP_OK
+        seen.append((out.clone(), one.clone()))
+        out.zero_(), one.zero_()
+    assert all(torch.equal(a, seen[0][0]) and torch.equal(b, seen[0][1]) for a, b in seen)
+    ref = packed.decode_attention_q8(dec(q[:1]), kq.cpu().numpy(), ks.cpu().numpy(), vq.cpu().numpy(),
+                                     vs.cpu().numpy(), [n], scale)
+    assert np.linalg.norm(seen[0][1].cpu().double().numpy() - ref) / np.linalg.norm(ref) <= 1e-5
+    z = torch.softmax(q[149, 0].double() @ kc[0, 0].double().T * scale, -1)
+    want, a = z @ vc[0, 0].double(), z @ vc[0, 0].double().abs()
+    got = seen[0][0][149, 0].double()
+    assert torch.all((got - want).abs() <= 2.0 ** -8 * (want.abs() + a) + 2.0 ** -11 * a)

@@ -639,8 +639,9 @@ bool attn_q8_shape_ok(int H, int H_kv) { return H % H_kv == 0 && H / H_kv <= 16;
 
 AttnLayout attn_q8_layout(int H, int H_kv, int D) {
   AttnLayout z;
-  z.counters = 256;
-  z.partials = z.counters + kQ8MaxCtas * sizeof(uint32_t);
+  static_assert(kQ8MaxCtas * sizeof(uint32_t) <= kPackedCounterBytes, "counters");
+  z.counters = kPackedCounters;
+  z.partials = z.counters + kPackedCounterBytes;
   z.total = z.partials + (size_t)2 * kQ8MaxCtas * (H / H_kv) * (3 + D) * sizeof(float);
   return z;
 }

@@ -608,7 +608,10 @@ fmlp_status fmlp_attn_decode_q8(const void* q, const void* k_q, const float* k_s
     if (!x || !aligned16(x)) return FMLP_ERR_INVALID_ARG;
   for (const void* x : {(const void*)k_s, (const void*)v_s, (const void*)kv_len})
     if (!x || !aligned4(x)) return FMLP_ERR_INVALID_ARG;
-  if (overlap(out, (uintptr_t)(B * H * D * 4), q, (uintptr_t)(B * H * D * 2)))
+  const uintptr_t out_bytes = (uintptr_t)(B * H * D * 4), rows = (uintptr_t)(B * H_kv * n_max);
+  if (overlap(out, out_bytes, q, (uintptr_t)(B * H * D * 2)) || overlap(out, out_bytes, k_q, rows * D) ||
+      overlap(out, out_bytes, v_q, rows * D) || overlap(out, out_bytes, k_s, rows * 4) ||
+      overlap(out, out_bytes, v_s, rows * 4))
     return FMLP_ERR_INVALID_ARG;
   const DeviceInfo* dev = nullptr;
   fmlp_status st = device_for_launch(&dev);

@@ -187,6 +187,10 @@ cudaError_t launch_kv_read_q8(const void* k_q, const float* k_s, const void* v_q
                               void* k_cache, void* v_cache, void* workspace, const DeviceInfo& dev,
                               cudaStream_t stream);
 
+// Arrival counters of the packed-batch attention calls, behind the control words of a
+// workspace: the same place and size in all of them (two a CTA at most), so that one
+// workspace serves them in any order.
+constexpr size_t kPackedCounters = 256, kPackedCounterBytes = 2 * 256 * sizeof(uint32_t);
 // Causal attention of a packed batch over its cache (csrc/prefill.cu).
 struct PrefillLayout {
   size_t counters = 0;  // arrivals at items split over CTAs (zero between calls)

@@ -835,8 +835,9 @@ bool prefill_shape_ok(int H, int H_kv) { return H % H_kv == 0 && H / H_kv <= kTi
 PrefillLayout prefill_layout(int64_t T, int H, int H_kv, int D) {
   PrefillLayout z;
   const int G = H / H_kv;
-  z.counters = 256;
-  z.partials = z.counters + 2 * kPfMaxCtas * sizeof(uint32_t);
+  static_assert(2 * kPfMaxCtas * sizeof(uint32_t) <= kPackedCounterBytes, "counters");
+  z.counters = kPackedCounters;
+  z.partials = z.counters + kPackedCounterBytes;
   z.total = z.partials + (size_t)2 * kPfMaxCtas * piece_tiles_of(T, G) * piece_rows_of(T, G) * (2 + D) * sizeof(float);
   return z;
 }
