@@ -25,6 +25,10 @@
 // kv_read_q8: rows [0, kv_len) of an int8 cache as bf16 (code times scale, in
 // f32, rounded once).  HBM-bound; every CTA walks 128-row tiles of all
 // (sequence, head) regions, lengths taken from the device.
+//
+// Measured on a B200: 8192 tokens of 32 + 8 + 8 heads of 128 with norms 38 us (5.3 TB/s,
+// 80% of the measured copy rate); 4235 tokens of 32 + 32 + 32 heads of 96 into an int8
+// cache of 9870 rows a head, read back, 77 us (4.1 TB/s); 8 tokens 2.9 us.
 #include "common.cuh"
 #include "internal.h"
 

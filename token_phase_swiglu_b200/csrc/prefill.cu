@@ -23,19 +23,30 @@
 //     S = Q K^T  (both operands in shared memory, f32 in TMEM)
 //     O += W V   (W bf16 in TMEM over the S it came from, V as a
 //                 column-major operand straight from its row-major tile)
-// and warps 0-3 and 4-7 hold one query row per thread of the two tiles: they
-// turn S into W while the tensor cores work on the other tile.  W is rounded to
-// bf16 (half a step, 2^-9 relative at most, averaged over the row's keys): it
-// must match V's type, and the output is bf16 as well.  l sums the unrounded w.
+// and warps 0-3 and 4-7 hold one query row per thread of the two tiles and turn S
+// into W.  The two 64-row halves of a unit have their own S and barriers: while the
+// products of one are under way (O += W V, then the next unit's S of that half), the
+// softmax works on the other.  W is rounded to bf16 (half a step, 2^-8 relative at
+// most): it must match V's type, and the output is bf16 as well.  l sums the
+// unrounded w.
 //
 // Schedule.  The 128-row units of all items (one KV tile against one pair of
-// query tiles) are split evenly and contiguously over the CTAs, a fixed cost for each
-// item's start and end counted with them, so a long cache
-// read by few tokens is spread over the whole GPU and ragged prompts balance.
+// query tiles) are split evenly and contiguously over the CTAs, a fixed cost for
+// each item's start and end counted with them (a prompt of 8192 tokens took 962 us
+// without it, 600 with), so a long cache read by few tokens is spread over the whole
+// GPU and ragged prompts balance.
 // An item cut by a CTA border leaves f32 pieces (m, l, O) in the workspace; the
 // last CTA to finish merges them in order (nobody waits on another CTA).  Every
 // CTA finds its first unit from the device-side lengths: the units of a
 // sequence are a sum of rounded-up arithmetic terms, which has a closed form.
+//
+// Measured on a B200 (32 query heads over 8 KV heads of 128): a prompt of 8192
+// tokens 511-550 us (1000-1075 TFLOP/s, under the power cap), of 2048 tokens 61 us
+// (566 TFLOP/s), 4 tokens of 32 sequences over caches of 4k rows 107 us (5.0 TB/s).
+// Prompts are bound by the products: scores of 64 rows at a time read shared memory
+// at its limit (48 cycles for 32 of work), but with 128 rows at once, which leaves no
+// room in TMEM for a second set, the softmax waits for them and the prompt of 8192
+// tokens takes 614 us.  Short ones are bound by starting and finishing items.
 #include "common.cuh"
 #include "internal.h"
 #include "plan.cuh"
@@ -671,6 +682,14 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
                           bf16x2(__uint_as_float(o[6]) * inv, __uint_as_float(o[7]) * inv));
       };
       tc_fence_after();
+      // The CTA that holds an item's start comes to it last of its own work, the others
+      // first of theirs: if they have all arrived it joins their pieces to its O as it is.
+      bool own = false;
+      if (cf != cl && (int)blockIdx.x == cf) {
+        if (r == 0) sh.last[t] = ld_acquire_gpu(p.counters + 2 * cf + t) == (uint32_t)(cl - cf);
+        named_barrier_sync(1 + t, kTile);
+        own = sh.last[t];
+      }
       if (cf == cl && ntok == TPT) {
         // a whole tile: through shared memory, 64 columns at a time, and one TMA store
         // (a thread's own row in 16-byte stores would touch 32 lines an instruction)
@@ -692,7 +711,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
           named_barrier_sync(1 + t, kTile);
           if (r == 0) tma_store_out(&p.o_map, stage, z * 64, w.g, w.s.c0 + first);
         }
-      } else if (warp_ok) {
+      } else if (warp_ok && !own) {
         float* pc = piece((int)blockIdx.x);
         if (cf != cl && row_ok) {
           pc[r] = m;
@@ -716,37 +735,52 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
           }
         }
       }
-      tc_fence_before();
       if (cf != cl) {
-        __threadfence();
-        named_barrier_sync(1 + t, kTile);
-        if (r == 0) sh.last[t] = atomicAdd(p.counters + 2 * cf + t, 1u) == (uint32_t)(cl - cf);
-        named_barrier_sync(1 + t, kTile);
+        if (!own) {
+          __threadfence();
+          named_barrier_sync(1 + t, kTile);
+          if (r == 0) sh.last[t] = atomicAdd(p.counters + 2 * cf + t, 1u) == (uint32_t)(cl - cf);
+          named_barrier_sync(1 + t, kTile);
+        }
         if (sh.last[t]) {
           __threadfence();
-          if (row_ok) {
-            float M = -CUDART_INF_F;
+          if (warp_ok) {
+            const int c0 = own ? cf + 1 : cf;  // the pieces in the workspace, in their order
+            const auto at = [&](int c, int i) { return __ldcg(piece(c) + i * p.piece_rows + r); };
+            float M = own ? m : -CUDART_INF_F, L = 0.f;
+            if (row_ok) {
 #pragma unroll 4
-            for (int c = cf; c <= cl; ++c) M = fmaxf(M, __ldcg(piece(c) + r));
+              for (int c = c0; c <= cl; ++c) M = fmaxf(M, at(c, 0));
+            }
             if (M == -CUDART_INF_F) M = 0.f;
-            float L = 0.f;
+            const float f0 = exp2f(m - M);
+            if (own) L = fmaf(f0, l, 0.f);  // as a piece's
+            if (row_ok) {
 #pragma unroll 4
-            for (int c = cf; c <= cl; ++c)
-              L = fmaf(exp2f(__ldcg(piece(c) + r) - M), __ldcg(piece(c) + p.piece_rows + r), L);
+              for (int c = c0; c <= cl; ++c) L = fmaf(exp2f(at(c, 0) - M), at(c, 1), L);
+            }
             const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 32) {  // 8 loads of each of two pieces in flight
               float acc[32];
+              if (own) {
+                uint32_t o[32];
+                load_o(d0, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+                for (int i = 0; i < 32; ++i) acc[i] = fmaf(f0, __uint_as_float(o[i]), 0.f);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+              }
+              if (!row_ok) continue;
 #pragma unroll 2
-              for (int c = cf; c <= cl; ++c) {
+              for (int c = c0; c <= cl; ++c) {
                 const float* pc = piece(c);
                 const float4* src = reinterpret_cast<const float4*>(pc + 2 * p.piece_rows) + (size_t)(d0 / 4) * p.piece_rows + r;
                 float4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + i * p.piece_rows);
-                const float f = exp2f(__ldcg(pc + r) - M);
+                const float f = exp2f(at(c, 0) - M);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                   acc[4 * i] = fmaf(f, v[i].x, acc[4 * i]);
@@ -766,6 +800,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
         }
         named_barrier_sync(1 + t, kTile);  // sh.last is written again
       }
+      tc_fence_before();
     }
     if (r == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
