@@ -326,8 +326,8 @@ FMLP_API fmlp_status fmlp_attn_decode(const void* q, const void* k_new, const vo
  *
  *   cu_seqlens : int32 [B + 1] on the device: sequence b has the new tokens
  *                t with cu_seqlens[b] <= t < cu_seqlens[b + 1] (none, one or
- *                many).  Tokens before cu_seqlens[0] or from cu_seqlens[B] on
- *                (a padded batch) are passed over: nothing is written for them.
+ *                many).  Tokens of no sequence (a padded batch) are passed
+ *                over: nothing is written for them.
  *   kv_len     : int32 [B] on the device: the rows that sequence b holds with
  *                its new tokens, 0 <= kv_len[b] <= n_max.  With n_b new tokens,
  *                its i-th one stands at position p = kv_len[b] - n_b + i, which
@@ -337,10 +337,13 @@ FMLP_API fmlp_status fmlp_attn_decode(const void* q, const void* k_new, const vo
  *                of them needs, serves all the packed-batch calls in any order;
  *                zero-fill it again after a call of another kind used it
  *                (fmlp_forward, fmlp_attn_decode, ...).  Read fmlp_device_status as for the other
- *                calls: a sequence whose kv_len is outside [0, n_max], or whose
- *                cu_seqlens decrease or leave [0, T], is not processed (its
- *                outputs and cache stay as they were) and is reported as
- *                FMLP_ERR_INVALID_ARG.
+ *                calls: a sequence b whose kv_len is outside [0, n_max], or whose
+ *                own cu_seqlens[b], cu_seqlens[b + 1] decrease or leave [0, T], is
+ *                not processed (its outputs and cache stay as they were) and is
+ *                reported as FMLP_ERR_INVALID_ARG; the others are processed.  (What
+ *                is written for a token that two of these share, after a
+ *                decrease, is unspecified.)  With T = 0 nothing is launched, so
+ *                nothing is reported.
  * The lengths are read on the device only, so a captured graph may be replayed
  * with other lengths in the same buffers.  All the calls run after the previous
  * work on `stream`, take H >= 1 query heads and H_kv >= 1 KV heads (at most

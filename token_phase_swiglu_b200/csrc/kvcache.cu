@@ -61,15 +61,48 @@ struct AppendParams {
   double freq[kMaxRopePairs], amplitude;
 };
 
-// The sequence of token t: the last b with cu[b] <= t.  A 32-ary search by
-// one warp (one step for up to 32 sequences).
+// Sequence b's lengths: new tokens [c0, c1) of the batch's T (the grid's first dimension),
+// len rows held with them.
+struct Lengths {
+  int c0, c1, len;
+  __device__ __forceinline__ Lengths(const AppendParams& p, int64_t b)
+      : c0(__ldg(p.cu + b)), c1(__ldg(p.cu + b + 1)), len(__ldg(p.kv_len + b)) {}
+  __device__ __forceinline__ bool ok(const AppendParams& p) const {
+    return c0 >= 0 && c0 <= c1 && c1 <= (int)gridDim.x && len >= 0 && len <= p.n_max;
+  }
+};
+// The first of the 32 N sequences from b0 on that may be processed and holds token t, by one
+// warp with all their lengths in one round trip: -1 if none does, with the token's position
+// in `pos` if one does.
+template <int N>
+__device__ __forceinline__ int64_t owner(const AppendParams& p, int64_t b0, int t, int lane, int& pos) {
+  bool mine[N];
+  int at[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t b = b0 + i * 32 + lane;
+    const Lengths s(p, min(b, p.B - 1));
+    mine[i] = b < p.B && s.ok(p) && s.c0 <= t && t < s.c1;
+    at[i] = mine[i] ? s.len - (s.c1 - t) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t found = __ballot_sync(0xffffffffu, mine[i]);
+    if (found) {
+      pos = __shfl_sync(0xffffffffu, at[i], __ffs(found) - 1);
+      return b0 + i * 32 + __ffs(found) - 1;
+    }
+  }
+  return -1;
+}
+// The last b with cu[b] <= t, if cu does not decrease (some b if it does).  A 32-ary search
+// by one warp.
 __device__ __forceinline__ int64_t sequence_of(const int32_t* cu, int64_t B, int64_t t, int lane) {
-  int64_t lo = 0, hi = B;  // cu[lo] <= t (checked by the caller), answer in [lo, hi)
+  int64_t lo = 0, hi = B;
   while (hi - lo > 1) {
     const int64_t step = (hi - lo + 31) / 32;
     const int64_t at = lo + lane * step;
     const bool le = at < hi && __ldg(cu + at) <= t;
-    // a malformed (decreasing) cu gives some b; the caller checks the range
     const int n = max(1, __popc(__ballot_sync(0xffffffffu, le)));
     lo += (int64_t)(n - 1) * step;
     hi = min(hi, lo + step);
@@ -122,30 +155,26 @@ __device__ __forceinline__ float group_max(float v) {
 }
 
 // Sequence and position of token t, by one warp: position -1 for a token that is passed
-// over (in no sequence, padding, or of a refused sequence).
-__device__ __forceinline__ int place(const AppendParams& p, int64_t t, int lane, int64_t& b) {
-  int64_t c0, c1, len;
-  if (p.B < 32) {  // every length in one round trip
-    const int64_t c = __ldg(p.cu + min((int64_t)lane, p.B));
-    const int64_t n = __ldg(p.kv_len + min((int64_t)lane, p.B - 1));
-    const int64_t first = __shfl_sync(0xffffffffu, c, 0), end = __shfl_sync(0xffffffffu, c, (int)p.B);
-    if (t < first || t >= end) return -1;
-    b = max(__popc(__ballot_sync(0xffffffffu, lane < p.B && c <= t)), 1) - 1;
-    c0 = __shfl_sync(0xffffffffu, c, (int)b);
-    c1 = __shfl_sync(0xffffffffu, c, (int)b + 1);
-    len = __shfl_sync(0xffffffffu, n, (int)b);
-  } else {
-    if (t < __ldg(p.cu) || t >= __ldg(p.cu + p.B)) return -1;
+// over (in no sequence, padding, or of a refused sequence).  Up to 256 sequences are all
+// asked at once, more are searched; a token that the search does not place is in none,
+// unless cu decreases somewhere, and then all are asked.
+constexpr int kAsked = 256;
+__device__ __forceinline__ int place(const AppendParams& p, int t, int lane, int64_t& b) {
+  int pos = -1;
+  if (p.B <= 32) {
+    b = owner<1>(p, 0, t, lane, pos);
+    return max(pos, -1);
+  }
+  if (p.B > kAsked) {
     b = sequence_of(p.cu, p.B, t, lane);
-    c0 = __ldg(p.cu + b);
-    c1 = __ldg(p.cu + b + 1);
-    len = __ldg(p.kv_len + b);
+    const Lengths s(p, b);
+    if (s.ok(p) && s.c0 <= t && t < s.c1) return max(s.len - (s.c1 - t), -1);
   }
-  if (t < c0 || t >= c1 || len < 0 || len > p.n_max) {
-    if (lane == 0) atomicOr(p.status, kStatusBadInput);
-    return -1;
+  for (int64_t b0 = 0; b0 < p.B; b0 += kAsked) {
+    b = owner<kAsked / 32>(p, b0, t, lane, pos);
+    if (b >= 0) break;
   }
-  return (int)max(len - (c1 - t), (int64_t)-1);
+  return max(pos, -1);
 }
 
 template <int D, bool kQ8>
@@ -191,11 +220,15 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append(const __grid_co
     }
     if (base == r0) {  // meanwhile: the token's place, then its cosines and sines
       if (tid < 32) {
-        const int at = place(p, t, tid, b);
+        const int at = place(p, (int)t, tid, b);
         if (tid == 0) {
           s_seq = b;
           s_pos = at;
         }
+      } else if (blockIdx.y == 0) {  // and by the other warps: lengths to be reported
+        constexpr int kOthers = kAppendThreads - 32;
+        for (int64_t i = (int64_t)blockIdx.x * kOthers + tid - 32; i < p.B; i += (int64_t)gridDim.x * kOthers)
+          if (!Lengths(p, i).ok(p)) atomicOr(p.status, kStatusBadInput);
       }
       __syncthreads();
       pos = s_pos;
