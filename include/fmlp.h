@@ -498,14 +498,17 @@ FMLP_API size_t fmlp_attn_q8_workspace_bytes(int64_t B, int H, int H_kv, int D);
  *
  *   q        : bf16 [B x H x D], already rotated
  *   k_q, v_q : int8 [B x H_kv x n_max x D] codes
- *   k_s, v_s : f32 [B x H_kv x n_max] scales, finite and >= 0; codes and scales of
- *              rows from kv_len[b] on may hold anything
+ *   k_s, v_s : f32 [B x H_kv x n_max] scales, finite and >= 0, or NaN (a row that
+ *              held a value that is not finite); codes and scales of rows from
+ *              kv_len[b] on may hold anything
  *   kv_len   : int32 [B] on the device; 0 gives zeros, a length outside [0, n_max]
  *              is not processed and reported as FMLP_ERR_INVALID_ARG
  *   scale    : > 0 and finite
  *   out      : f32 [B x H x D], of f32 precision: the codes are multiplied exactly
  *              (integer tensor cores) with queries held to 2^-20 and softmax weights to
  *              2^-24 of their largest.  The same bits on every run with the same lengths.
+ *              A head with a NaN or an infinity in its query, or that sees a row with a
+ *              NaN scale, gets NaN; no other head does.
  *   workspace: fmlp_attn_q8_workspace_bytes(B, H, H_kv, D), not shared by calls that
  *              may overlap on the GPU.  After a call that reported FMLP_ERR_TIMEOUT,
  *              zero it again before reuse.

@@ -329,16 +329,21 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
       if (s >= 2 && !wait(&sh.q_empty[buf], s / 2 - 1)) break;
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
-        float top = 0.f;
+        float top = 0.f, zero = 0.f;  // zero becomes NaN with a value that is not finite
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) top = fmaxf(top, fabsf(x[h][i]));
+        for (int i = 0; i < D / 32; ++i) {
+          top = fmaxf(top, fabsf(x[h][i]));
+          zero = fmaf(x[h][i], 0.f, zero);
+        }
         top = warp_top(top);
+        const bool finite = __all_sync(0xffffffffu, zero == 0.f);
         // over a power of two, so that the largest lies in [32, 64)
         const uint32_t e = max((__float_as_uint(top) >> 23) & 255u, 6u);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
           split3(tl.q[buf], 3 * h, i * 32 + lane, x[h][i] * __uint_as_float((259u - e) << 23), kBaseQ);
-        if (lane == 0) tl.q_scale[buf][h] = __uint_as_float((e - 5u) << 23) * p.scale_log2;
+        // digits cannot say NaN: the scale does, and every score and sum of the head with it
+        if (lane == 0) tl.q_scale[buf][h] = finite ? __uint_as_float((e - 5u) << 23) * p.scale_log2 : CUDART_NAN_F;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&sh.q_full[buf]);
@@ -459,12 +464,13 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
           const bool valid = (w.j0 + i) * kU + r < w.len;
           const float ks = scales[r], vs = scales[kU + r];
           const float lv = valid ? __log2f(vs) : -CUDART_INF_F;
+          const float one = fmaf(vs, 0.f, 1.f);  // NaN for a scale of V that is not finite
 #pragma unroll
           for (int h = 0; h < GP; ++h) {
             sc[h] = join3(a[3 * h], a[3 * h + 1], a[3 * h + 2], kBaseQ) * qs[h] * ks;
             if (valid) {  // running maximum and sum of this thread's rows
               const float d = sc[h] - m[h], e = ex2(-fabsf(d));
-              l[h] = d > 0.f ? fmaf(l[h], e, 1.f) : l[h] + e;
+              l[h] = d > 0.f ? fmaf(l[h], e, one) : fmaf(e, one, l[h]);
               m[h] = fmaxf(m[h], sc[h]);
             }
             exps[h] = valid ? sc[h] + lv : -CUDART_INF_F;
