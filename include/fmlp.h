@@ -420,7 +420,9 @@ FMLP_API fmlp_status fmlp_rope_append(const void* q, int64_t q_stride, const voi
  *     s = fl32(max |x| / 127)
  * and D int8 codes rint(x * fl32(1 / s)), within +-127, taken from the f32
  * values after norm and rotation.  A row stands for codes * s, which is within
- * (0.5 + 2^-15) s of x.  A row whose s would be under 2^-125 is held as zeros.
+ * (0.5 + 2^-15) s of x.  A row whose s would be under 2^-125 is held as zeros;
+ * one with a NaN or an infinity (after norm and rotation) gets NaN as its scale,
+ * so that it is read back and attended to as NaN.
  *
  *   k_q, v_q : int8 [B x H_kv x n_max x D]
  *   k_s, v_s : f32 [B x H_kv x n_max]

@@ -83,3 +83,74 @@ def test_row_scale(fm, cuda_device, lens, H, H_kv, D, n_max, which):
                 assert torch.all(torch.isnan(got[b, g * group:(g + 1) * group]))
                 got[b, g * group:(g + 1) * group] = want[b, g * group:(g + 1) * group]
             assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("D,R,norms", [(64, 64, False), (96, 48, True), (128, 128, False), (128, 0, True)])
+def test_append(fm, cuda_device, D, R, norms):
+    """A value of k or v that is not finite: its row's scale is NaN, the other rows keep their bits;
+    read back and attended to, the row is NaN."""
+    H, H_kv, n, held = 4, 2, 6, 9
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    x = {c: wl.normal_bf16(D, 81 + i, (n, h, D)).to(cuda_device) for i, (c, h) in enumerate((("q", H), ("k", H_kv), ("v", H_kv)))}
+    gamma = wl.normal_bf16(D, 84, (D,), mean=1.0, std=0.2).to(cuda_device) if norms else None
+    ws = torch.zeros(fm.fmlp_attn_q8_workspace_bytes(1, H, H_kv, D), dtype=torch.uint8, device=cuda_device)
+
+    def append(**kw):
+        a, q_out = x | kw, torch.zeros(n, H, D, dtype=torch.bfloat16, device=cuda_device)
+        c = {"k_q": torch.ones(1, H_kv, held, D, dtype=torch.int8, device=cuda_device),
+             "v_q": torch.ones(1, H_kv, held, D, dtype=torch.int8, device=cuda_device),
+             "k_s": torch.ones(1, H_kv, held, device=cuda_device), "v_s": torch.ones(1, H_kv, held, device=cuda_device)}
+        fm.fmlp_rope_append_q8(a["q"], a["k"], a["v"], i32([0, n]), i32([held]), fm.FmlpRope(1e4, R), q_out, c["k_q"],
+                               c["k_s"], c["v_q"], c["v_s"], ws, q_gamma=gamma, k_gamma=gamma)
+        assert fm.fmlp_device_status(ws) == fm.FMLP_OK
+        return q_out, c
+
+    q_out, want = append()
+    assert all(torch.all(torch.isfinite(t)) for t in (q_out, want["k_s"], want["v_s"]))
+    big = 3e38                                                    # a pair of them may turn past the largest number
+    for which in "kv":
+        for i, bad in enumerate((NAN, INF, -INF, big)):
+            t, g, d = (2 * i + 1) % n, i % H_kv, (29 * i + 3) % D
+            y = x[which].clone()
+            y[t, g, d] = bad
+            if bad == big:
+                y[t, g] = big
+            q2, got = append(**{which: y})
+            row = held - n + t
+            seen = which == "k" or bad != big                     # a row of v is copied, and 3e38 / 127 is a scale
+            if which == "k" and bad == big:
+                seen = bool(torch.isnan(got["k_s"][0, g, row]))   # by its angles
+                assert seen or torch.isfinite(got["k_s"][0, g, row])
+            assert torch.equal(q2, q_out)
+            assert bool(torch.isnan(got[which + "_s"][0, g, row])) == seen
+            bf = {c: torch.zeros(1, H_kv, held, D, dtype=torch.bfloat16, device=cuda_device) for c in "kv"}
+            fm.fmlp_kv_read_q8(got["k_q"], got["k_s"], got["v_q"], got["v_s"], i32([held]), bf["k"], bf["v"], ws)
+            assert bool(torch.all(torch.isnan(bf[which][0, g, row]))) == seen
+            out = torch.zeros(1, H, D, device=cuda_device)
+            fm.fmlp_attn_decode_q8(q_out[-1:], got["k_q"], got["k_s"], got["v_q"], got["v_s"], i32([held]),
+                                   1 / math.sqrt(D), out, ws)
+            if seen:
+                assert torch.all(torch.isnan(out[0].view(H_kv, -1)[g])) and torch.all(torch.isfinite(out[0].view(H_kv, -1)[1 - g]))
+            for c in want:                                        # the other rows
+                a, b = got[c].clone(), want[c].clone()
+                if c[0] == which:
+                    a[0, g, row], b[0, g, row] = 0, 0
+                assert torch.equal(a, b)
+
+
+def test_append_query(fm, cuda_device):
+    """q is not quantised: NaN and infinity stay where the rotation puts them."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    q = torch.ones(2, 2, 64, dtype=torch.bfloat16, device=cuda_device)
+    q[0, 1, 3], q[1, 0, 40] = NAN, INF
+    k = torch.ones(2, 1, 64, dtype=torch.bfloat16, device=cuda_device)
+    c = [torch.zeros(1, 1, 2, 64, dtype=torch.int8, device=cuda_device) for _ in range(2)]
+    sc = [torch.zeros(1, 1, 2, device=cuda_device) for _ in range(2)]
+    ws = torch.zeros(256, dtype=torch.uint8, device=cuda_device)
+    out = torch.zeros_like(q)
+    fm.fmlp_rope_append_q8(q, k, k, i32([0, 2]), i32([2]), fm.FmlpRope(1e4, 64), out, c[0], sc[0], c[1], sc[1], ws)
+    bad = ~torch.isfinite(out)
+    want = torch.zeros_like(bad)
+    want[0, 1, [3, 35]] = True
+    want[1, 0, [8, 40]] = True
+    assert torch.equal(bad, want) and all(torch.all(torch.isfinite(t)) for t in sc)

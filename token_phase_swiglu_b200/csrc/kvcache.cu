@@ -32,6 +32,8 @@
 #include "common.cuh"
 #include "internal.h"
 
+#include <math_constants.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -147,10 +149,15 @@ __device__ __forceinline__ float group_sum(float v) {
   for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = L / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -291,9 +298,11 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append(const __grid_co
       if (kQ8) {
         float m = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(x0.x[j]), fabsf(x1.x[j])));
+        for (int j = 0; j < 8; ++j) m = max_nan(m, max_nan(fabsf(x0.x[j]), fabsf(x1.x[j])));
         s = __fdiv_rn(group_max<L>(m), 127.f);
-        if (s < 0x1p-125f)
+        if (!(s < CUDART_INF_F))
+          s = CUDART_NAN_F;  // codes cannot hold a NaN or an infinity: the scale says so
+        else if (s < 0x1p-125f)
           s = 0.f;  // its reciprocal may overflow
         else
           inv = __frcp_rn(s);
