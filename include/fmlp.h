@@ -418,9 +418,9 @@ FMLP_API fmlp_status fmlp_rope_append(const void* q, int64_t q_stride, const voi
  * fmlp_rope_append_q8 -- the same into an int8 cache, this library's own
  * format: each row x (D values of one head) is held as one binary32 scale
  *     s = fl32(max |x| / 127)
- * and D int8 codes rint(x * fl32(1 / s)), within +-127, taken from the f32
+ * and D int8 codes rint(x / s) (ties to even), within +-127, taken from the f32
  * values after norm and rotation.  A row stands for codes * s, which is within
- * (0.5 + 2^-15) s of x.  A row whose s would be under 2^-125 is held as zeros;
+ * s / 2 of x.  A row whose s would be under 2^-125 is held as zeros;
  * one with a NaN or an infinity (after norm and rotation) gets NaN as its scale,
  * so that it is read back and attended to as NaN.
  *

@@ -10,8 +10,8 @@
 //     once; the rotation itself is f32;
 //   * q is rounded to bf16 into q_out; k and v go to row p of their head's
 //     cache region, as bf16 (v a bit copy), or as int8 codes with one f32
-//     scale a row: s = fl32(max |x| / 127), code = rint(x fl32(1 / s)), taken
-//     from the f32 values, so a key is rounded once.
+//     scale a row: s = fl32(max |x| / 127), code = rint(x / s), taken from the
+//     f32 values, so a key is rounded once.
 // Bound by HBM for prompts (each row read once and written once) and by the
 // latency of one launch for decode steps.
 //
@@ -130,14 +130,29 @@ __device__ __forceinline__ uint4 pack(const Chunk& c) {
   return make_uint4(pack2(c.x[0], c.x[1]), pack2(c.x[2], c.x[3]), pack2(c.x[4], c.x[5]),
                     pack2(c.x[6], c.x[7]));
 }
-// rint(x * inv) of 8 values as bytes (|x * inv| < 127.5): adding 1.5 * 2^23 to the exact
-// product rounds it to an integer whose two's complement is in the low bits.  (Dividing
-// each value by the scale instead made the kernel bound by its instructions.)
-__device__ __forceinline__ uint2 codes(const Chunk& c, float inv) {
+// rint(x / s) of 8 values as bytes (|x / s| < 127.5), ties to even, with inv = fl32(1 / s):
+// adding 1.5 * 2^23 to the exact product x inv rounds it to an integer whose two's complement
+// is in the low bits.  That is rint(x / s) unless the quotient stands next to a half, which
+// the remainder x - code s, exact in f32, says.  (Dividing each value by the scale made the
+// kernel bound by its instructions; looking twice at the rare rest costs 2%.)
+__device__ __forceinline__ uint2 codes(const Chunk& c, float s, float inv) {
   constexpr float kMagic = 12582912.f;
+  const float half = s > 0.f ? 0.5f * s : CUDART_INF_F;  // none for rows of zeros (or NaN)
   uint32_t t[8];
+  bool near_half = false;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) t[j] = __float_as_uint(fmaf(c.x[j], inv, kMagic));
+  for (int j = 0; j < 8; ++j) {
+    const float y = fmaf(c.x[j], inv, kMagic);
+    t[j] = __float_as_uint(y);
+    near_half |= fabsf(fmaf(kMagic - y, s, c.x[j])) >= half;
+  }
+  if (near_half) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float rest = fmaf(kMagic - __uint_as_float(t[j]), s, c.x[j]), a = fabsf(rest);
+      if (a > half || (a == half && (t[j] & 1u))) t[j] += rest < 0.f ? -1 : 1;
+    }
+  }
   const auto join = [&](int i) {
     return __byte_perm(__byte_perm(t[i], t[i + 1], 0x0040), __byte_perm(t[i + 2], t[i + 3], 0x0040), 0x5410);
   };
@@ -315,8 +330,8 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append(const __grid_co
         *reinterpret_cast<uint4*>(dst + 8 * c1) = pack(x1);
       } else if (kQ8) {
         int8_t* dst = (is_v ? p.v_q : p.k_q) + row * D;
-        *reinterpret_cast<uint2*>(dst + 8 * c0) = codes(x0, inv);
-        *reinterpret_cast<uint2*>(dst + 8 * c1) = codes(x1, inv);
+        *reinterpret_cast<uint2*>(dst + 8 * c0) = codes(x0, s, inv);
+        *reinterpret_cast<uint2*>(dst + 8 * c1) = codes(x1, s, inv);
         if (u == 0) (is_v ? p.v_s : p.k_s)[row] = s;
       } else {
         __nv_bfloat16* dst = (is_v ? p.v_cache : p.k_cache) + row * D;
