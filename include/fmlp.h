@@ -507,10 +507,11 @@ FMLP_API size_t fmlp_attn_q8_workspace_bytes(int64_t B, int H, int H_kv, int D);
  *              is not processed and reported as FMLP_ERR_INVALID_ARG
  *   scale    : > 0 and finite
  *   out      : f32 [B x H x D], of f32 precision: the codes are multiplied exactly
- *              (integer tensor cores) with queries held to 2^-20 and softmax weights to
- *              2^-24 of their largest.  The same bits on every run with the same lengths.
- *              A head with a NaN or an infinity in its query, or that sees a row with a
- *              NaN scale, gets NaN; no other head does.
+ *              (integer tensor cores) with a head's queries held to 2^-30 of their
+ *              largest (2^-128 if that is under 2^-98) and softmax weights to 2^-24 of
+ *              theirs.  The same bits on every run with the same lengths.  A head with
+ *              a NaN or an infinity in its query, or that sees a row with a NaN scale,
+ *              gets NaN; no other head does.
  *   workspace: fmlp_attn_q8_workspace_bytes(B, H, H_kv, D), not shared by calls that
  *              may overlap on the GPU.  After a call that reported FMLP_ERR_TIMEOUT,
  *              zero it again before reuse.

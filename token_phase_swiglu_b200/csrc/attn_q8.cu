@@ -6,10 +6,12 @@
 // integer sums), so no thread ever unpacks a cache byte:
 //     S^T[j, h] = K_j . Q_h      A = 128 rows of K, as stored (row-major)
 //     O^T[d, h] = V^T[d, .] W_h  A = V transposed by the operand descriptor
-// The few queries are the narrow operand.  A query value (over a power of two near
-// its head's largest) and a softmax weight (over its unit's largest) are split into
-// three int8 digits, 3 columns a head, joined in f32 after the product: queries to
-// 2^-20 of the largest (a bf16 value within 2^13 of it exactly), weights to 2^-24.
+// The few queries are the narrow operand.  A query value, over a power of two near its
+// head's largest, is split into four int8 digits and a softmax weight, over its unit's
+// largest, into three, as many columns a head, joined in f32 after the product: queries
+// to 2^-30 of the largest (a bf16 value whose exponent is up to 22 lower exactly, so that
+// an outlier does not coarsen the rest: three digits, the same width for up to 8 heads a KV
+// head, would hold 2^-22), weights to 2^-24.
 // With the scales,
 //     s_j = (S^T joined) * power * ks_j * scale * log2 e,
 //     weight of V's codes: 2^(s_j + log2 vs_j - M), M the unit's largest exponent,
@@ -73,7 +75,9 @@ struct Q8Params {
   int slots;
 };
 
-__host__ __device__ constexpr int q8_cols(int GP) { return (3 * GP + 15) / 16 * 16; }  // columns of a product
+// Columns of the score products (4 digits a head) and of those with V (3).
+__host__ __device__ constexpr int q8_q_cols(int GP) { return (4 * GP + 15) / 16 * 16; }
+__host__ __device__ constexpr int q8_w_cols(int GP) { return (3 * GP + 15) / 16 * 16; }
 
 template <int GP>
 struct Q8Shared {
@@ -87,8 +91,8 @@ struct Q8Shared {
 // what the groups exchange.
 template <int GP>
 struct Q8Tiles {
-  uint8_t q[2][q8_cols(GP) * 128];  // of the current segment and the next one
-  uint8_t w[2][q8_cols(GP) * 128];  // of the two groups' units
+  uint8_t q[2][q8_q_cols(GP) * 128];  // of the current segment and the next one
+  uint8_t w[2][q8_w_cols(GP) * 128];  // of the two groups' units
   float acc[GP * kU];               // group 1's, joined by group 0
   float q_scale[2][GP];
   float top[2][2][4][GP];           // largest exponents: group, unit parity, warp
@@ -134,23 +138,34 @@ __device__ __forceinline__ float warp_top(float v) {
 __device__ __forceinline__ int tile_byte(int n, int c) {
   return n * 128 + (((c >> 4) ^ (n & 7)) << 4) + (c & 15);
 }
+// The four digits of an integer |x| <= 2^30 into rows n .. n + 3 of column c, lowest first,
+// each within [-128, 127]: with 128 added to the lower three, they are the bytes of a sum.
+__device__ __forceinline__ void split4(uint8_t* tile, int n, int c, int x) {
+  const uint32_t d = ((uint32_t)x + 0x00808080u) ^ 0x00808080u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tile[tile_byte(n + i, c)] = (uint8_t)(d >> (8 * i));
+}
+// Their sums joined, in units of the highest digit.
+__device__ __forceinline__ float join4(const uint32_t* s) {
+  constexpr float kStep = 0x1p-8f;
+  return fmaf(fmaf(fmaf((float)(int)s[0], kStep, (float)(int)s[1]), kStep, (float)(int)s[2]), kStep, (float)(int)s[3]);
+}
 // The three digits of y in [-127, 127] into rows n, n + 1, n + 2 of column c: y0 = rint(y),
-// then what is left, times the base, twice.  Base 128 keeps a query's binary digits
-// (an exact split of a bf16 value over a power of two); base 254 is the largest whose
-// digits stay within +-127, for weights.  Adding 1.5 * 2^23 rounds to an integer whose
-// two's complement is in the low bits.
-constexpr float kBaseQ = 128.f, kBaseW = 254.f;
-__device__ __forceinline__ void split3(uint8_t* tile, int n, int c, float y, float base) {
+// then what is left, times the base, twice.  Base 254 is the largest whose digits stay
+// within +-127.  Adding 1.5 * 2^23 rounds to an integer whose two's complement is in the
+// low bits.
+constexpr float kBase = 254.f;
+__device__ __forceinline__ void split3(uint8_t* tile, int n, int c, float y) {
   constexpr float kMagic = 12582912.f;
-  const float b0 = y + kMagic, r1 = (y - (b0 - kMagic)) * base;
-  const float b1 = r1 + kMagic, r2 = (r1 - (b1 - kMagic)) * base;
+  const float b0 = y + kMagic, r1 = (y - (b0 - kMagic)) * kBase;
+  const float b1 = r1 + kMagic, r2 = (r1 - (b1 - kMagic)) * kBase;
   const float b2 = r2 + kMagic;
   tile[tile_byte(n, c)] = (uint8_t)__float_as_uint(b0);
   tile[tile_byte(n + 1, c)] = (uint8_t)__float_as_uint(b1);
   tile[tile_byte(n + 2, c)] = (uint8_t)__float_as_uint(b2);
 }
-__device__ __forceinline__ float join3(uint32_t a, uint32_t b, uint32_t c, float base) {
-  return fmaf(fmaf((float)(int)c, 1.f / base, (float)(int)b), 1.f / base, (float)(int)a);
+__device__ __forceinline__ float join3(const uint32_t* s) {
+  return fmaf(fmaf((float)(int)s[2], 1.f / kBase, (float)(int)s[1]), 1.f / kBase, (float)(int)s[0]);
 }
 // 2^(a - b), with 2^(-inf - anything) = 0
 __device__ __forceinline__ float ex2_diff(float a, float b) {
@@ -216,15 +231,16 @@ struct Q8Walk {
 template <int D, int GP>
 __global__ void __launch_bounds__(kQ8Threads, 1)
 attn_decode_q8(const __grid_constant__ Q8Params p) {
-  constexpr int N = q8_cols(GP);
-  constexpr uint32_t kTmemCols = N == 16 ? 64 : N == 32 ? 128 : 256;  // S and O of two groups
+  constexpr int NS = q8_q_cols(GP), NO = q8_w_cols(GP);  // columns of S and O
+  constexpr uint32_t kTmemCols = GP <= 4 ? 64 : GP <= 8 ? 128 : 256;  // S, then O, of two groups
+  static_assert(2 * (NS + NO) <= (int)kTmemCols, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Q8Shared<GP>& sh = *reinterpret_cast<Q8Shared<GP>*>(smem);
   Q8Tiles<GP>& tl = *reinterpret_cast<Q8Tiles<GP>*>(smem + kQ8Header);
   uint8_t* ring = smem + kQ8Header + (sizeof(Q8Tiles<GP>) + 1023) / 1024 * 1024;
   static_assert(sizeof(Q8Shared<GP>) <= kQ8Header, "header");
-  static_assert(q8_cols(GP) * 128 % 1024 == 0, "operand tiles are whole swizzle atoms");
+  static_assert(NS % 8 == 0 && NO % 8 == 0, "operand tiles are whole swizzle atoms");
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -245,7 +261,7 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
     fence_barrier_init();
   }
   for (int i = threadIdx.x; i < (int)sizeof(tl.w) / 4; i += kQ8Threads)
-    reinterpret_cast<uint32_t*>(&tl.w[0][0])[i] = 0;  // columns past 3 GP stay zero
+    reinterpret_cast<uint32_t*>(&tl.w[0][0])[i] = 0;  // columns of no digit stay zero
   for (int i = threadIdx.x; i < (int)sizeof(tl.q) / 4; i += kQ8Threads)
     reinterpret_cast<uint32_t*>(&tl.q[0][0])[i] = 0;
   if (warp == kQ8Mma) tmem_alloc(&sh.tmem, kTmemCols);
@@ -337,11 +353,12 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
         }
         top = warp_top(top);
         const bool finite = __all_sync(0xffffffffu, zero == 0.f);
-        // over a power of two, so that the largest lies in [32, 64)
-        const uint32_t e = max((__float_as_uint(top) >> 23) & 255u, 6u);
+        // over a power of two, so that the largest lies in [2^29, 2^30); heads under 2^-98 are
+        // all taken over 2^-127
+        const uint32_t e = max((__float_as_uint(top) >> 23) & 255u, 29u);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-          split3(tl.q[buf], 3 * h, i * 32 + lane, x[h][i] * __uint_as_float((259u - e) << 23), kBaseQ);
+          split4(tl.q[buf], 4 * h, i * 32 + lane, __float2int_rn(x[h][i] * __uint_as_float((283u - e) << 23)));
         // digits cannot say NaN: the scale does, and every score and sum of the head with it
         if (lane == 0) tl.q_scale[buf][h] = finite ? __uint_as_float((e - 5u) << 23) * p.scale_log2 : CUDART_NAN_F;
       }
@@ -354,7 +371,7 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
     // ---------------- MMA issuer (one lane) ----------------
     if (elect_one()) {
       Q8Walk w;
-      const uint32_t idesc = idesc_i8(N);
+      const uint32_t idesc_s = idesc_i8(NS), idesc_o = idesc_i8(NO) | kTransposeA;
       const uint32_t ring_lo = operand(smem_u32(ring));
       const uint32_t q_lo[2] = {operand(smem_u32(tl.q[0])), operand(smem_u32(tl.q[1]))};
       const uint32_t w_lo[2] = {operand(smem_u32(tl.w[0])), operand(smem_u32(tl.w[1]))};
@@ -374,10 +391,10 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
         if (!(ok = wait_one(&sh.full[slot], kq / p.slots))) return;
         tc_fence_after();
         const bool last = i + 1 == w.count();
-        const uint32_t a = ring_lo + slot * (kQ8SlotBytes >> 4), b = q_lo[s & 1], d = tmem + (kq & 1) * N;
-        mma_i8<false>(d, a, b, idesc);
+        const uint32_t a = ring_lo + slot * (kQ8SlotBytes >> 4), b = q_lo[s & 1], d = tmem + (kq & 1) * NS;
+        mma_i8<false>(d, a, b, idesc_s);
 #pragma unroll
-        for (int c = 1; c < D / 32; ++c) mma_i8<true>(d, a + c * 2, b + c * 2, idesc);
+        for (int c = 1; c < D / 32; ++c) mma_i8<true>(d, a + c * 2, b + c * 2, idesc_s);
         mma_commit(&sh.s_full[kq & 1]);
         if (last) mma_commit(&sh.q_empty[s & 1]);
         ++kq;
@@ -395,10 +412,10 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
         if (!(ok = wait_one(&sh.p_full[wg], k >> 1))) break;
         tc_fence_after();
         const uint32_t a = ring_lo + slot * (kQ8SlotBytes >> 4) + (kQ8TileBytes >> 4), b = w_lo[wg];
-        const uint32_t d = tmem + (2 + wg) * N;
-        mma_i8<false>(d, a, b, idesc | kTransposeA);
+        const uint32_t d = tmem + 2 * NS + wg * NO;
+        mma_i8<false>(d, a, b, idesc_o);
 #pragma unroll
-        for (int c = 1; c < kU / 32; ++c) mma_i8<true>(d, a + c * (4096 >> 4), b + c * 2, idesc | kTransposeA);
+        for (int c = 1; c < kU / 32; ++c) mma_i8<true>(d, a + c * (4096 >> 4), b + c * 2, idesc_o);
         mma_commit(&sh.o_full[wg]);
         mma_commit(&sh.empty[slot]);
         next_qk();  // W of unit k is in, so its S has been read
@@ -440,13 +457,13 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
         ok = wait(&sh.o_full[wg], mine - 1);
         if (!ok) return;
         tc_fence_after();
-        uint32_t o[N];
-        tmem_ld_cols<N>(tmem + lanes + (2 + wg) * N, o);
+        uint32_t o[NO];
+        tmem_ld_cols<NO>(tmem + lanes + 2 * NS + wg * NO, o);
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
           const float nref = fmaxf(ref[h], top[h]);
           acc[h] = acc[h] * ex2_diff(ref[h], nref) +
-                   join3(o[3 * h], o[3 * h + 1], o[3 * h + 2], kBaseW) * ex2_diff(top[h], nref);
+                   join3(o + 3 * h) * ex2_diff(top[h], nref);
           ref[h] = nref;
         }
       };
@@ -456,18 +473,21 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
         if (ok) ok = wait(&sh.full[slot], k / p.slots) && wait(&sh.s_full[wg], mine);
         float sc[GP], exps[GP];
         if (ok) {
-          __syncwarp();
           tc_fence_after();
-          uint32_t a[N];
-          tmem_ld_cols<N>(tmem + lanes + wg * N, a);
           const float* scales = reinterpret_cast<const float*>(ring + (size_t)slot * kQ8SlotBytes + 2 * kQ8TileBytes);
           const bool valid = (w.j0 + i) * kU + r < w.len;
           const float ks = scales[r], vs = scales[kU + r];
           const float lv = valid ? __log2f(vs) : -CUDART_INF_F;
           const float one = fmaf(vs, 0.f, 1.f);  // NaN for a scale of V that is not finite
+          constexpr int kPart = NS < 32 ? NS : 32;  // columns read at a time
+          uint32_t a[kPart];
 #pragma unroll
           for (int h = 0; h < GP; ++h) {
-            sc[h] = join3(a[3 * h], a[3 * h + 1], a[3 * h + 2], kBaseQ) * qs[h] * ks;
+            if (h % (kPart / 4) == 0) {
+              __syncwarp();
+              tmem_ld_cols<kPart>(tmem + lanes + wg * NS + 4 * h, a);
+            }
+            sc[h] = join4(a + 4 * h % kPart) * qs[h] * ks;
             if (valid) {  // running maximum and sum of this thread's rows
               const float d = sc[h] - m[h], e = ex2(-fabsf(d));
               l[h] = d > 0.f ? fmaf(l[h], e, one) : fmaf(e, one, l[h]);
@@ -489,7 +509,7 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
           for (int h = 0; h < GP; ++h) {
             const float(*t)[GP] = tl.top[wg][mine & 1];
             top[h] = fmaxf(fmaxf(t[0][h], t[1][h]), fmaxf(t[2][h], t[3][h]));
-            split3(tl.w[wg], 3 * h, r, 127.f * ex2_diff(exps[h], top[h]), kBaseW);
+            split3(tl.w[wg], 3 * h, r, 127.f * ex2_diff(exps[h], top[h]));
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           tc_fence_before();
