@@ -666,7 +666,8 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
         return p.partials + ((size_t)slot * p.piece_tiles + t) * p.piece_rows * (2 + D);
       };
       const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-      const auto load_o = [&](int c, uint32_t (&o)[32]) {  // columns c .. c + 31
+      const auto load_o = [&](int c, uint32_t (&o)[32]) {  // columns c .. c + 31, by whole warps
+        __syncwarp();  // lanes without a row pass over the stores of the columns before
         if (any) {
           tmem_ld<32>(o_addr + c, o);
           tmem_wait();
@@ -721,11 +722,10 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           load_o(c, o);
-          if (!row_ok) continue;
-          if (cf == cl) {
+          if (row_ok && cf == cl) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(out + c + i) = pack8(o + i);
-          } else {
+          } else if (row_ok) {
             float4* dst = reinterpret_cast<float4*>(pc + 2 * p.piece_rows);
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -772,28 +772,29 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) acc[i] = 0.f;
               }
-              if (!row_ok) continue;
+              if (row_ok) {
 #pragma unroll 2
-              for (int c = c0; c <= cl; ++c) {
-                const float* pc = piece(c);
-                const float4* src = reinterpret_cast<const float4*>(pc + 2 * p.piece_rows) + (size_t)(d0 / 4) * p.piece_rows + r;
-                float4 v[8];
+                for (int c = c0; c <= cl; ++c) {
+                  const float* pc = piece(c);
+                  const float4* src = reinterpret_cast<const float4*>(pc + 2 * p.piece_rows) + (size_t)(d0 / 4) * p.piece_rows + r;
+                  float4 v[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + i * p.piece_rows);
-                const float f = exp2f(at(c, 0) - M);
+                  for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + i * p.piece_rows);
+                  const float f = exp2f(at(c, 0) - M);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  acc[4 * i] = fmaf(f, v[i].x, acc[4 * i]);
-                  acc[4 * i + 1] = fmaf(f, v[i].y, acc[4 * i + 1]);
-                  acc[4 * i + 2] = fmaf(f, v[i].z, acc[4 * i + 2]);
-                  acc[4 * i + 3] = fmaf(f, v[i].w, acc[4 * i + 3]);
+                  for (int i = 0; i < 8; ++i) {
+                    acc[4 * i] = fmaf(f, v[i].x, acc[4 * i]);
+                    acc[4 * i + 1] = fmaf(f, v[i].y, acc[4 * i + 1]);
+                    acc[4 * i + 2] = fmaf(f, v[i].z, acc[4 * i + 2]);
+                    acc[4 * i + 3] = fmaf(f, v[i].w, acc[4 * i + 3]);
+                  }
                 }
-              }
 #pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4*>(out + d0 + i) =
-                    make_uint4(bf16x2(acc[i] * inv, acc[i + 1] * inv), bf16x2(acc[i + 2] * inv, acc[i + 3] * inv),
-                               bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), bf16x2(acc[i + 6] * inv, acc[i + 7] * inv));
+                for (int i = 0; i < 32; i += 8)
+                  *reinterpret_cast<uint4*>(out + d0 + i) =
+                      make_uint4(bf16x2(acc[i] * inv, acc[i + 1] * inv), bf16x2(acc[i + 2] * inv, acc[i + 3] * inv),
+                                 bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), bf16x2(acc[i + 6] * inv, acc[i + 7] * inv));
+              }
             }
           }
           if (r == 0) atomicExch(p.counters + 2 * cf + t, 0u);
