@@ -351,7 +351,9 @@ FMLP_API fmlp_status fmlp_attn_decode(const void* q, const void* k_new, const vo
  * 0 <= T <= 2^24 tokens and n_max < 2^30 rows, and return
  * FMLP_ERR_INVALID_ARG before launching anything for arguments outside what
  * they take.  Pointers are 16-byte aligned (cu_seqlens, kv_len and scales:
- * 4-byte).
+ * 4-byte).  What a call writes (outputs, cache rows and scales, the workspace)
+ * must not overlap what it reads nor each other, unless a call says so; a strided
+ * input counts from its first row's start to its last row's end, a cache whole.
  */
 #define FMLP_CONTROL_BYTES ((size_t)256)
 
@@ -399,7 +401,7 @@ typedef struct fmlp_rope {
  *                gamma over the D values of each head, before the rotation
  *   eps        : > 0 and finite (read only if a gamma is given)
  *   q_out      : bf16 [T x H x D], the rotated queries.  It may be q itself
- *                (q_stride = H D); it must not overlap q, k or v otherwise.
+ *                (q_stride = H D).
  *   k_cache,
  *   v_cache    : bf16 [B x H_kv x n_max x D]; rows p of the new tokens are
  *                written, every other row stays as it was
@@ -470,9 +472,8 @@ FMLP_API size_t fmlp_prefill_workspace_bytes(int64_t T, int64_t B, int H, int H_
  *               values, the rows behind may hold anything
  *   scale     : > 0 and finite (1/sqrt(D) usually)
  *   out       : bf16 [T x H x D], rounded once from f32 sums; the softmax
- *               weights are rounded to bf16 for their product with V.  It must
- *               not overlap q or the caches.  The same bits on every run with
- *               the same lengths.
+ *               weights are rounded to bf16 for their product with V.  The same
+ *               bits on every run with the same lengths.
  *   workspace : fmlp_prefill_workspace_bytes(T, B, H, H_kv, D), not shared by
  *               calls that may overlap on the GPU.  After a call that reported
  *               FMLP_ERR_TIMEOUT, zero it again before reuse.

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 
 namespace fmlp {
@@ -471,6 +472,31 @@ static bool rows_ok(const void* x, int64_t stride, int64_t row) {
   return x && aligned16(x) && stride >= row && stride % 8 == 0 && stride <= (int64_t)1 << 30;
 }
 
+// Memory that a call reads or writes (none at all if `p` is null).
+struct Range {
+  const void* p;
+  uintptr_t bytes;
+};
+static bool overlap(const Range& a, const Range& b) {
+  return (uintptr_t)a.p < (uintptr_t)b.p + b.bytes && (uintptr_t)b.p < (uintptr_t)a.p + a.bytes;
+}
+// Whether an output shares memory with an input or with another output: other threads of
+// the same launch would read or write it at the same time.
+static bool any_overlap(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  for (const Range* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Range* other = o + 1; other != outs.end(); ++other)
+      if (overlap(*o, *other)) return true;
+    for (const Range& in : ins)
+      if (overlap(*o, in)) return true;
+  }
+  return false;
+}
+// A cache's regions of `row` bytes a row (more rows than any memory holds count as 2^50).
+static Range regions(const void* p, int64_t B, int H_kv, int64_t n_max, int64_t row) {
+  return {p, (uintptr_t)(std::min<int64_t>(B * H_kv * n_max, (int64_t)1 << 50) * row)};
+}
+static Range vec32(const void* p, int64_t n) { return {p, (uintptr_t)n * 4}; }
+
 static fmlp_status append_impl(const AppendArgs& a, size_t workspace_bytes, void* stream) {
   if (!batch_ok(a.B, a.H, a.H_kv, a.D, a.n_max) || !tokens_ok(a.T)) return FMLP_ERR_INVALID_ARG;
   if (!control_ok(a.workspace, workspace_bytes)) return FMLP_ERR_INVALID_ARG;
@@ -487,16 +513,24 @@ static fmlp_status append_impl(const AppendArgs& a, size_t workspace_bytes, void
       !rows_ok(a.k, a.k_stride, (int64_t)a.H_kv * a.D) ||
       !rows_ok(a.v, a.v_stride, (int64_t)a.H_kv * a.D) || !a.q_out || !aligned16(a.q_out))
     return FMLP_ERR_INVALID_ARG;
-  // q_out may be q itself; otherwise it overlaps no row that another thread reads
-  const uintptr_t o0 = (uintptr_t)a.q_out, o1 = o0 + (uintptr_t)a.T * a.H * a.D * 2;
-  const struct { const void* x; int64_t stride, row; } in[3] = {
-      {a.q, a.q_stride, (int64_t)a.H * a.D}, {a.k, a.k_stride, (int64_t)a.H_kv * a.D},
-      {a.v, a.v_stride, (int64_t)a.H_kv * a.D}};
-  for (const auto& x : in) {
-    const uintptr_t x0 = (uintptr_t)x.x, x1 = x0 + (uintptr_t)((a.T - 1) * x.stride + x.row) * 2;
-    const bool same = &x == in && o0 == x0 && x.stride == x.row;
-    if (o0 < x1 && x0 < o1 && !same) return FMLP_ERR_INVALID_ARG;
-  }
+  const auto rows = [&](const void* x, int64_t stride, int64_t row) -> Range {
+    return {x, (uintptr_t)((a.T - 1) * stride + row) * 2};
+  };
+  const int64_t q_row = (int64_t)a.H * a.D, kv_row = (int64_t)a.H_kv * a.D, d = a.k_s ? a.D : 2 * a.D;
+  // q_out may be q itself: each lane writes the pieces that it read
+  const bool in_place = a.q_out == a.q && a.q_stride == q_row;
+  if (any_overlap({{a.q_out, (uintptr_t)(a.T * q_row * 2)},
+                   regions(a.k_cache, a.B, a.H_kv, a.n_max, d),
+                   regions(a.v_cache, a.B, a.H_kv, a.n_max, d),
+                   regions(a.k_s, a.B, a.H_kv, a.n_max, a.k_s ? 4 : 0),
+                   regions(a.v_s, a.B, a.H_kv, a.n_max, a.v_s ? 4 : 0),
+                   {a.workspace, FMLP_CONTROL_BYTES}},
+                  {in_place ? Range{} : rows(a.q, a.q_stride, q_row),
+                   rows(a.k, a.k_stride, kv_row), rows(a.v, a.v_stride, kv_row),
+                   vec32(a.cu_seqlens, a.B + 1), vec32(a.kv_len, a.B),
+                   {a.q_gamma, a.q_gamma ? (uintptr_t)a.D * 2 : 0},
+                   {a.k_gamma, a.k_gamma ? (uintptr_t)a.D * 2 : 0}}))
+    return FMLP_ERR_INVALID_ARG;
   const DeviceInfo* dev = nullptr;
   fmlp_status st = device_for_launch(&dev);
   if (st != FMLP_OK) return st;
@@ -540,16 +574,17 @@ fmlp_status fmlp_kv_read_q8(const void* k_q, const float* k_s, const void* v_q, 
     if (!x || !aligned16(x)) return FMLP_ERR_INVALID_ARG;
   if (!k_s || !v_s || !kv_len || !aligned4(k_s) || !aligned4(v_s) || !aligned4(kv_len))
     return FMLP_ERR_INVALID_ARG;
+  if (any_overlap({regions(k_cache, B, H_kv, n_max, 2 * D), regions(v_cache, B, H_kv, n_max, 2 * D),
+                   {workspace, FMLP_CONTROL_BYTES}},
+                  {regions(k_q, B, H_kv, n_max, D), regions(v_q, B, H_kv, n_max, D),
+                   regions(k_s, B, H_kv, n_max, 4), regions(v_s, B, H_kv, n_max, 4), vec32(kv_len, B)}))
+    return FMLP_ERR_INVALID_ARG;
   const DeviceInfo* dev = nullptr;
   fmlp_status st = device_for_launch(&dev);
   if (st != FMLP_OK) return st;
   cudaError_t e = launch_kv_read_q8(k_q, k_s, v_q, v_s, kv_len, B, H_kv, D, n_max, k_cache, v_cache,
                                     workspace, *dev, (cudaStream_t)stream);
   return e == cudaSuccess ? FMLP_OK : cuda_fail(e);
-}
-
-static bool overlap(const void* a, uintptr_t a_bytes, const void* b, uintptr_t b_bytes) {
-  return (uintptr_t)a < (uintptr_t)b + b_bytes && (uintptr_t)b < (uintptr_t)a + a_bytes;
 }
 
 size_t fmlp_prefill_workspace_bytes(int64_t T, int64_t B, int H, int H_kv, int D) {
@@ -575,10 +610,10 @@ fmlp_status fmlp_attn_prefill(const void* q, int64_t q_stride, const void* k_cac
   if (T == 0) return FMLP_OK;
   const int64_t row = (int64_t)H * D;
   if (!rows_ok(q, q_stride, row) || !out || !aligned16(out)) return FMLP_ERR_INVALID_ARG;
-  const uintptr_t out_bytes = (uintptr_t)(T * row * 2);
-  const uintptr_t cache_bytes = (uintptr_t)(B * H_kv * n_max * D * 2);
-  if (overlap(out, out_bytes, q, (uintptr_t)((T - 1) * q_stride + row) * 2) ||
-      overlap(out, out_bytes, k_cache, cache_bytes) || overlap(out, out_bytes, v_cache, cache_bytes))
+  if (any_overlap({{out, (uintptr_t)(T * row * 2)}, {workspace, prefill_layout(T, H, H_kv, D).total}},
+                  {{q, (uintptr_t)((T - 1) * q_stride + row) * 2},
+                   regions(k_cache, B, H_kv, n_max, 2 * D), regions(v_cache, B, H_kv, n_max, 2 * D),
+                   vec32(cu_seqlens, B + 1), vec32(kv_len, B)}))
     return FMLP_ERR_INVALID_ARG;
   const DeviceInfo* dev = nullptr;
   fmlp_status st = device_for_launch(&dev);
@@ -608,10 +643,10 @@ fmlp_status fmlp_attn_decode_q8(const void* q, const void* k_q, const float* k_s
     if (!x || !aligned16(x)) return FMLP_ERR_INVALID_ARG;
   for (const void* x : {(const void*)k_s, (const void*)v_s, (const void*)kv_len})
     if (!x || !aligned4(x)) return FMLP_ERR_INVALID_ARG;
-  const uintptr_t out_bytes = (uintptr_t)(B * H * D * 4), rows = (uintptr_t)(B * H_kv * n_max);
-  if (overlap(out, out_bytes, q, (uintptr_t)(B * H * D * 2)) || overlap(out, out_bytes, k_q, rows * D) ||
-      overlap(out, out_bytes, v_q, rows * D) || overlap(out, out_bytes, k_s, rows * 4) ||
-      overlap(out, out_bytes, v_s, rows * 4))
+  if (any_overlap({{out, (uintptr_t)(B * H * D * 4)}, {workspace, attn_q8_layout(H, H_kv, D).total}},
+                  {{q, (uintptr_t)(B * H * D * 2)}, regions(k_q, B, H_kv, n_max, D),
+                   regions(v_q, B, H_kv, n_max, D), regions(k_s, B, H_kv, n_max, 4),
+                   regions(v_s, B, H_kv, n_max, 4), vec32(kv_len, B)}))
     return FMLP_ERR_INVALID_ARG;
   const DeviceInfo* dev = nullptr;
   fmlp_status st = device_for_launch(&dev);
