@@ -620,7 +620,9 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
             if (j == w.j0 && h == 0) {
               m = top;
-            } else if (__any_sync(0xffffffffu, top > m + kRescaleAbove)) {
+            } else if (__any_sync(0xffffffffu, row_ok && top > m + kRescaleAbove)) {
+              // (rows of no token have no say: where 128 is not a multiple of G the last ones
+              // meet whatever shared memory held, and a result would depend on it)
               // this S came after the product with W of two halves ago, so only the last
               // one's can be pending (the phase waited for is the barrier's or the one before)
               if (!(ok = wait(&sh.pv_done[t], ns[0] + ns[1] - 2))) continue;
