@@ -57,7 +57,10 @@ constexpr int kQ8SlotBytes = 2 * kQ8TileBytes + 1024;  // K, V, then both rows o
 constexpr int kQ8Header = 1024;
 constexpr int kQ8MaxCtas = 256;
 // A region costs its units and, to start and to finish, about as much as this many
-// more; the shares of the CTAs are counted in both.
+// more; the shares of the CTAs are counted in both.  4 against 2 and 8: 8 sequences of up to
+// 8k rows, 8 KV heads of 128 with 4 heads each 28.3 us (29.4, 28.4), 32 with one 59.6 (59.6,
+// 61.0), of 64 with 4 heads 25.9 (26.9, 25.9), with one 52.2 (52.3, 54.0), with 16 34.8
+// (40.6, 34.3).
 constexpr int kRegionCost = 4;
 
 struct Q8Params {
@@ -104,17 +107,13 @@ __device__ __forceinline__ uint32_t idesc_i8(int N) {  // int8 x int8 -> int32, 
   return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kU >> 4) << 24);
 }
 constexpr uint32_t kTransposeA = 1u << 15;
-// Operand tiles have rows of 128 bytes with the 128-byte swizzle, groups of 8 rows 1024
-// bytes apart; a descriptor is this constant upper word and a lower one with the address.
-constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t operand(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 template <bool kAccumulate>
 __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
       " setp.ne.b32 p, %5, 0;\n"
       " tcgen05.mma.cta_group::1.kind::i8 [%0], a, b, %4, p;\n}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "n"(kOperandHi), "r"(idesc), "n"((int)kAccumulate));
+      "r"(a_lo), "r"(b_lo), "n"(kSw128DescHi), "r"(idesc), "n"((int)kAccumulate));
 }
 __device__ __forceinline__ void tma_load_rows(void* dst, const void* tmap, int y, int z, uint64_t* bar,
                                               uint64_t policy) {
@@ -372,9 +371,9 @@ attn_decode_q8(const __grid_constant__ Q8Params p) {
     if (elect_one()) {
       Q8Walk w;
       const uint32_t idesc_s = idesc_i8(NS), idesc_o = idesc_i8(NO) | kTransposeA;
-      const uint32_t ring_lo = operand(smem_u32(ring));
-      const uint32_t q_lo[2] = {operand(smem_u32(tl.q[0])), operand(smem_u32(tl.q[1]))};
-      const uint32_t w_lo[2] = {operand(smem_u32(tl.w[0])), operand(smem_u32(tl.w[1]))};
+      const uint32_t ring_lo = sw128_desc_lo(smem_u32(ring));
+      const uint32_t q_lo[2] = {sw128_desc_lo(smem_u32(tl.q[0])), sw128_desc_lo(smem_u32(tl.q[1]))};
+      const uint32_t w_lo[2] = {sw128_desc_lo(smem_u32(tl.w[0])), sw128_desc_lo(smem_u32(tl.w[1]))};
       const auto wait_one = [&](uint64_t* bar, int phase) {
         if (mbar_wait_bounded(bar, (uint32_t)(phase & 1), p.ctl.wait_ns, abort)) return true;
         sh.abort = 1;

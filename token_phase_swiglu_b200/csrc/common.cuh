@@ -172,6 +172,13 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Two values rounded to bf16 (to nearest even), `lo` in the lower half.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+
 // 2^x by the hardware approximation (relative error 2^-22; 0 for x = -inf).
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -121,14 +121,9 @@ __device__ __forceinline__ Chunk unpack(uint4 w) {
   c.x[4] = bf16lo(w.z); c.x[5] = bf16hi(w.z); c.x[6] = bf16lo(w.w); c.x[7] = bf16hi(w.w);
   return c;
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t w;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  return w;
-}
 __device__ __forceinline__ uint4 pack(const Chunk& c) {
-  return make_uint4(pack2(c.x[0], c.x[1]), pack2(c.x[2], c.x[3]), pack2(c.x[4], c.x[5]),
-                    pack2(c.x[6], c.x[7]));
+  return make_uint4(bf16x2(c.x[0], c.x[1]), bf16x2(c.x[2], c.x[3]), bf16x2(c.x[4], c.x[5]),
+                    bf16x2(c.x[6], c.x[7]));
 }
 // rint(x / s) of 8 values as bytes (|x / s| < 127.5), ties to even, with inv = fl32(1 / s):
 // adding 1.5 * 2^23 to the exact product x inv rounds it to an integer whose two's complement
@@ -411,8 +406,8 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_q8(const __grid_constant
               const float f1 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7441)) - 8388736.f;
               const float f2 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7442)) - 8388736.f;
               const float f3 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7443)) - 8388736.f;
-              o[2 * i4] = pack2(f0 * s, f1 * s);
-              o[2 * i4 + 1] = pack2(f2 * s, f3 * s);
+              o[2 * i4] = bf16x2(f0 * s, f1 * s);
+              o[2 * i4 + 1] = bf16x2(f2 * s, f3 * s);
             }
             uint4* dst = reinterpret_cast<uint4*>((kv ? p.v_out : p.k_out) + r0 * D) + 2 * e;
             dst[0] = make_uint4(o[0], o[1], o[2], o[3]);

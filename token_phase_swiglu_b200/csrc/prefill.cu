@@ -72,7 +72,9 @@ constexpr int kPfMaxCtas = 256;
 constexpr int kPfHeader = 1024;
 constexpr float kRescaleAbove = 8.f;
 // An item costs its units and, to start (Q, the first K) and to finish (O), about as
-// much as this many more; the shares of the CTAs are counted in both.
+// much as this many more; the shares of the CTAs are counted in both.  2 against 1 and 4:
+// five prompts of up to 1500 tokens, 16 heads of 128 over 4 70.3 us (71.9, 73.4), over 16
+// 81.5 (83.7, 82.4); of 64 54.1 (52.8, 58.2) and 56.9 (55.5, 60.1).
 constexpr int kPfItemCost = 2;
 // TMEM columns: S of the two tiles in halves of 64 (W over the first 32 of each), O of them
 constexpr uint32_t kColS = 0, kColO = 256, kPfTmemCols = 512;
@@ -244,14 +246,8 @@ __device__ __forceinline__ void tma_load_q(void* dst, const void* tmap, int x, i
       ::"r"(smem_u32(dst)), "l"(tmap), "r"(x), "r"(0), "r"(g), "r"(t), "r"(smem_u32(bar)) : "memory");
 }
 
-// Operand descriptors, as their constant upper and address-bearing lower words: an
-// operand further on is one addition to the lower word (16-byte units), so that the
-// issuing thread keeps ahead of the tensor cores (building each descriptor anew took
-// longer than its product).  V as the B operand: element (k = row, n = column) of
-// row-major rows of 64 columns (128 bytes, swizzled), groups of 8 rows 1024 bytes
-// apart, blocks of 64 columns kPfBlock apart.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_k_major(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+// V as the B operand: element (k = row, n = column) of row-major rows of 64 columns (128
+// bytes, swizzled), groups of 8 rows 1024 bytes apart, blocks of 64 columns kPfBlock apart.
 __device__ __forceinline__ uint32_t desc_v(uint32_t saddr) {
   return (saddr >> 4) | ((uint32_t)(kPfBlock >> 4) << 16);
 }
@@ -264,14 +260,14 @@ __device__ __forceinline__ void pf_mma(uint32_t d_tmem, uint32_t a_lo, uint32_t 
       "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
       " setp.ne.b32 p, %5, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "n"(kDescHi), "r"(idesc), "n"((int)kAccumulate));
+      "r"(a_lo), "r"(b_lo), "n"(kSw128DescHi), "r"(idesc), "n"((int)kAccumulate));
 }
 __device__ __forceinline__ void pf_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate));
+      "r"(a_tmem), "r"(b_lo), "n"(kSw128DescHi), "r"(idesc), "r"(accumulate));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -294,11 +290,6 @@ __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ void unpk2(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t w;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  return w;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -461,7 +452,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
       int np[2][2] = {{0, 0}, {0, 0}};  // W halves consumed
       bool ok = true;
       constexpr uint32_t kIdescS = idesc_bf16(kTile / 2), kIdescO = idesc_bf16(D) | kTransposeB;
-      const uint32_t q_lo = desc_k_major(smem_u32(q_smem)), kv_addr = smem_u32(kv_smem);
+      const uint32_t q_lo = sw128_desc_lo(smem_u32(q_smem)), kv_addr = smem_u32(kv_smem);
       const auto wait = [&](uint64_t* bar, int phase) {
         if (mbar_wait_bounded(bar, (uint32_t)(phase & 1), wait_ns, abort)) return true;
         sh.abort = 1;
@@ -470,7 +461,7 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
       };
       const auto qk = [&](int t, int h, int slot) {  // half h of S_t = Q_t K^T
         const uint32_t a = q_lo + t * (kTileBytes >> 4);
-        const uint32_t b = desc_k_major(kv_addr + slot * kTileBytes + h * (kPfBlock / 2));
+        const uint32_t b = sw128_desc_lo(kv_addr + slot * kTileBytes + h * (kPfBlock / 2));
         const uint32_t d = tmem + kColS + t * kTile + h * 64;
         pf_mma<false>(d, a, b, kIdescS);
 #pragma unroll

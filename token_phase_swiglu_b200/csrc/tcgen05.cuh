@@ -26,6 +26,12 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   return d;
 }
 
+// The same as its constant upper and address-bearing lower words: an operand further on is
+// one addition to the lower word (16-byte units), so that the issuing thread keeps ahead of
+// the tensor cores (building each descriptor anew took longer than its product).
+constexpr uint32_t kSw128DescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+
 // Instruction descriptor: bf16 x bf16 -> f32, A and B K-major, M = 128, N.
 __host__ __device__ constexpr uint32_t idesc_bf16(int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
