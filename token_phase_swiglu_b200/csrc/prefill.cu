@@ -568,23 +568,26 @@ attn_prefill(const __grid_constant__ PrefillParams p) {
       bool ok = true;
       for (int j = w.j0; j < jend && ok; ++j) {
         const int held = w.s.len - j * kTile;
-        if (held < kTile) {
-          // V's rows past the sequence's end may hold anything, and 0 * NaN is NaN: zeroed
-          // before this tile's products (tiles arrive K, V, K, V, ..., by unit)
-          const int n = 2 * (unit0 + j - w.j0) + 1, slot = n % p.slots;
-          if (!(ok = wait(&sh.kv_full[slot], n / p.slots))) break;
-          uint4* v = reinterpret_cast<uint4*>(kv_smem + slot * kTileBytes);
-          for (int z = 0; z < kBlocks; ++z)
-            for (int i = held * 8 + r; i < kTile * 8; i += kTile)
-              v[z * (kPfBlock / 16) + i] = make_uint4(0, 0, 0, 0);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         const int halves = w.halves(t, j);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h >= halves || !ok) continue;
           if (!(ok = wait(&sh.s_full[t][h], ns[h]))) continue;
           ++ns[h];
+          if (h == 0 && held < kTile) {
+            // V's rows past the sequence's end may hold anything, and 0 * NaN is NaN: zeroed
+            // before this tile's products (tiles arrive K, V, K, V, ..., by unit).  Only now:
+            // this unit's S says that all tiles before its K have arrived, so that the wait is
+            // for this V.  Before, a group that had no part in some units could be so far
+            // ahead that the barrier's last phase but one looked like the one waited for.
+            const int n = 2 * (unit0 + j - w.j0) + 1, slot = n % p.slots;
+            if (!(ok = wait(&sh.kv_full[slot], n / p.slots))) continue;
+            uint4* v = reinterpret_cast<uint4*>(kv_smem + slot * kTileBytes);
+            for (int z = 0; z < kBlocks; ++z)
+              for (int i = held * 8 + r; i < kTile * 8; i += kTile)
+                v[z * (kPfBlock / 16) + i] = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
           if (warp_ok) {
             tc_fence_after();
             uint32_t s[64];
