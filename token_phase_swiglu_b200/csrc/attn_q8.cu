@@ -30,8 +30,10 @@
 // border leaves f32 pieces in the workspace, merged in order by the last CTA.
 //
 // Measured on a B200: 16 sequences of up to 16k rows, 32 query heads over 8 KV heads of
-// 128, 66 us (5.2 TB/s of cache, 79% of the measured copy rate); one sequence of 4096
+// 128, 66-68 us (5.1 TB/s of cache, 78% of the measured copy rate); one sequence of 4096
 // rows, 32 heads of 96, 15 us, where launch, lengths, first tiles and merge take most.
+// At D = 64 a unit moves half the bytes through the same chain of waits: 8 sequences of up
+// to 8k rows, 32 heads each with its KV head, 52 us (3.4 TB/s) against 59.6 us (5.8) of 128.
 #include "common.cuh"
 #include "internal.h"
 #include "plan.cuh"

@@ -28,7 +28,7 @@
 //
 // Measured on a B200: 8192 tokens of 32 + 8 + 8 heads of 128 with norms 38 us (5.3 TB/s,
 // 80% of the measured copy rate); 4235 tokens of 32 + 32 + 32 heads of 96 into an int8
-// cache of 9870 rows a head, read back, 77 us (4.1 TB/s); 8 tokens 2.9 us.
+// cache of 9870 rows a head, read back, 81 us (3.9 TB/s); 8 tokens 2.8 us.
 #include "common.cuh"
 #include "internal.h"
 

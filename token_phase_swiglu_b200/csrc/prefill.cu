@@ -40,9 +40,10 @@
 // CTA finds its first unit from the device-side lengths: the units of a
 // sequence are a sum of rounded-up arithmetic terms, which has a closed form.
 //
-// Measured on a B200 (32 query heads over 8 KV heads of 128): a prompt of 8192
-// tokens 511-550 us (1000-1075 TFLOP/s, under the power cap), of 2048 tokens 61 us
-// (566 TFLOP/s), 4 tokens of 32 sequences over caches of 4k rows 107 us (5.0 TB/s).
+// Measured on a B200 (32 query heads over 8 KV heads of 128; back to back in a graph, and
+// as one pass among others): a prompt of 8192 tokens 508-565 and 580 us (1080-950 TFLOP/s,
+// under the power cap), of 2048 tokens 60 and 60 us (570 TFLOP/s), 4 tokens of 32 sequences
+// over caches of 4k rows 107 and 121 us (5.0 and 4.5 TB/s).
 // Prompts are bound by the products: scores of 64 rows at a time read shared memory
 // at its limit (48 cycles for 32 of work), but with 128 rows at once, which leaves no
 // room in TMEM for a second set, the softmax waits for them and the prompt of 8192
