@@ -26,9 +26,9 @@
 // f32, rounded once).  HBM-bound; every CTA walks 128-row tiles of all
 // (sequence, head) regions, lengths taken from the device.
 //
-// Measured on a B200: 8192 tokens of 32 + 8 + 8 heads of 128 with norms 38 us (5.3 TB/s,
-// 80% of the measured copy rate); 4235 tokens of 32 + 32 + 32 heads of 96 into an int8
-// cache of 9870 rows a head, read back, 81 us (3.9 TB/s); 8 tokens 2.8 us.
+// Measured on a B200: 8192 tokens of 32 + 8 + 8 heads of 128 with norms 37 us (5.4 TB/s,
+// 83% of the measured copy rate); 4235 tokens of 32 + 32 + 32 heads of 96 into an int8
+// cache of 9870 rows a head, read back, 80 us (4.0 TB/s); 8 tokens 2.8 us.
 #include "common.cuh"
 #include "internal.h"
 
@@ -172,25 +172,35 @@ __device__ __forceinline__ float group_max(float v) {
 }
 
 // Sequence and position of token t, by one warp: position -1 for a token that is passed
-// over (in no sequence, padding, or of a refused sequence).  Up to 256 sequences are all
-// asked at once, more are searched; a token that the search does not place is in none,
-// unless cu decreases somewhere, and then all are asked.
-constexpr int kAsked = 256;
+// over (in no sequence, padding, or of a refused sequence), kUnplaced if the search among
+// more than 32 sequences does not find one that holds it.  Then it is in none, unless cu
+// decreases somewhere; a token that some of cu's entries lie before and some behind is then
+// looked for in all sequences (place_anywhere).
+constexpr int kUnplaced = -2;
 __device__ __forceinline__ int place(const AppendParams& p, int t, int lane, int64_t& b) {
-  int pos = -1;
   if (p.B <= 32) {
+    int pos = -1;
     b = owner<1>(p, 0, t, lane, pos);
     return max(pos, -1);
   }
-  if (p.B > kAsked) {
-    b = sequence_of(p.cu, p.B, t, lane);
-    const Lengths s(p, b);
-    if (s.ok(p) && s.c0 <= t && t < s.c1) return max(s.len - (s.c1 - t), -1);
-  }
-  for (int64_t b0 = 0; b0 < p.B; b0 += kAsked) {
-    b = owner<kAsked / 32>(p, b0, t, lane, pos);
-    if (b >= 0) break;
-  }
+  b = sequence_of(p.cu, p.B, t, lane);
+  const Lengths s(p, b);
+  return s.ok(p) && s.c0 <= t && t < s.c1 ? max(s.len - (s.c1 - t), -1) : kUnplaced;
+}
+// Which sides of t the entries first, first + step, ... of cu lie on: bit 0 if some are behind
+// it or at it, bit 1 if some are before it.  If all of them lie on one side, no sequence holds
+// t (the tokens of a padded batch).
+__device__ __forceinline__ int sides(const AppendParams& p, int t, int64_t first, int step) {
+  int found = 0;
+  for (int64_t i = first; i <= p.B; i += step) found |= __ldg(p.cu + i) <= t ? 1 : 2;
+  return found;
+}
+// Sequence and position by asking all sequences, by one warp (64 at a time: 32 and 256 made
+// the rest of the kernel slower, 39.4 and 38.3 us against 37.2 for 8192 tokens).
+__device__ __forceinline__ int place_anywhere(const AppendParams& p, int t, int lane, int64_t& b) {
+  int pos = -1;
+  b = -1;
+  for (int64_t b0 = 0; b0 < p.B && b < 0; b0 += 64) b = owner<2>(p, b0, t, lane, pos);
   return max(pos, -1);
 }
 
@@ -201,7 +211,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append(const __grid_co
   constexpr int kGroups = kAppendThreads / L;
   __shared__ float cs[kMaxRopePairs], sn[kMaxRopePairs];
   __shared__ int64_t s_seq;
-  __shared__ int s_pos;
+  __shared__ int s_pos, s_sides[kAppendThreads / 32];
 
   grid_launch_dependents();
   grid_dependency_wait();  // every input may come from the previous kernel
@@ -236,18 +246,41 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append(const __grid_co
       }
     }
     if (base == r0) {  // meanwhile: the token's place, then its cosines and sines
+      constexpr int kOthers = kAppendThreads - 32;
+      const bool few = p.B < 4 * kOthers;  // cu's sides looked at beside the search, not after it
       if (tid < 32) {
         const int at = place(p, (int)t, tid, b);
         if (tid == 0) {
           s_seq = b;
           s_pos = at;
         }
-      } else if (blockIdx.y == 0) {  // and by the other warps: lengths to be reported
-        constexpr int kOthers = kAppendThreads - 32;
-        for (int64_t i = (int64_t)blockIdx.x * kOthers + tid - 32; i < p.B; i += (int64_t)gridDim.x * kOthers)
-          if (!Lengths(p, i).ok(p)) atomicOr(p.status, kStatusBadInput);
+      } else {
+        if (few && p.B > 32) {
+          const int both = __reduce_or_sync(0xffffffffu, sides(p, (int)t, tid - 32, kOthers));
+          if (tid % 32 == 0) s_sides[tid / 32] = both;
+        }
+        if (blockIdx.y == 0) {  // lengths to be reported
+          for (int64_t i = (int64_t)blockIdx.x * kOthers + tid - 32; i < p.B; i += (int64_t)gridDim.x * kOthers)
+            if (!Lengths(p, i).ok(p)) atomicOr(p.status, kStatusBadInput);
+        }
       }
       __syncthreads();
+      if (s_pos == kUnplaced) {
+        if (!few) {
+          const int both = __reduce_or_sync(0xffffffffu, sides(p, (int)t, tid, kAppendThreads));
+          if (tid % 32 == 0) s_sides[tid / 32] = both;
+          __syncthreads();
+        }
+        if (((few ? 0 : s_sides[0]) | s_sides[1] | s_sides[2] | s_sides[3]) != 3) return;
+        if (tid < 32) {
+          const int at = place_anywhere(p, (int)t, tid, b);
+          if (tid == 0) {
+            s_seq = b;
+            s_pos = at;
+          }
+        }
+        __syncthreads();
+      }
       pos = s_pos;
       if (pos < 0) return;
       b = s_seq;
