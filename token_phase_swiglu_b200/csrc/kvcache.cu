@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append(const __grid_co
           __syncthreads();
         }
         if (((few ? 0 : s_sides[0]) | s_sides[1] | s_sides[2] | s_sides[3]) != 3) return;
+        __syncthreads();  // every thread has seen s_pos before it is written again
         if (tid < 32) {
           const int at = place_anywhere(p, (int)t, tid, b);
           if (tid == 0) {
